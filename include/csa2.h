@@ -290,6 +290,109 @@ csa2_status csa2_sparse_attn_decode_nvfp4(const void *q_bf16, int32_t nq, int32_
 size_t csa2_sparse_attn_nvfp4_workspace_size(int32_t nq, int32_t h, int32_t k, int32_t w_max);
 
 /*
+ * Page operators of the paged cache (no counterpart in the pages; [P3] "CSA2
+ * tackles storage" makes one cache serve all layers, so a sequence's state is
+ * its page-table row and its length). Sequences may share physical pages:
+ * refs [rows_cap / page_size] (device array owned by the caller, here and for
+ * the other int32 arrays of these calls 4-byte aligned) counts the sequences
+ * that hold each page, 0 meaning free. A
+ * sequence holds the first ceil(seq_len / page_size) pages of its row, the
+ * rest of the row is -1. These calls write kv->page_table, kv->seq_len and
+ * refs, which every other call only reads.
+ *
+ * Every result follows from the arguments alone: entries of a call count in
+ * their order, pages are taken lowest first among those free before the call
+ * (pages that the call itself releases are free afterwards). An entry that
+ * cannot be served is skipped as a whole and sets CSA2_DEVERR_PAGES: a
+ * sequence outside the batch, one that an earlier entry of the call names as
+ * child or seq, a child that is not empty or is its own parent, a length that
+ * is negative or does not fit the row, a cut page outside the cache, or no
+ * free pages (then every later entry that needs pages is skipped too).
+ *
+ * copy_src, copy_dst [n] (both or neither may be NULL): the page that entry i
+ * copied (in part) and its copy, or -1. With several caches behind one page
+ * table (one per Full layer) the call serves the first one and
+ * csa2_pages_copy, given these lists, the others (its whole-page copy covers
+ * the part).
+ *
+ * csa2_pages_copy: pages src[i] -> dst[i] (codes, scales and, when kidx is
+ *   not NULL, keys), i < n; -1 in either list is an empty slot and a page to
+ *   itself nothing to do; a page outside the cache is skipped and sets
+ *   CSA2_DEVERR_BAD_ROW. No page may be written twice or be both written and
+ *   read (its bytes would be a mix).
+ * csa2_pages_fork: child[i], an empty sequence, becomes the first
+ *   min(length[i], seq_len[parent[i]]) entries of parent[i] (length NULL: all
+ *   of them). Whole pages are shared; the used rows of a partial last page are
+ *   copied to a page of the child's own, so that appends to either sequence
+ *   never touch the other. Lengths are those before the call: a child of this
+ *   call is an empty parent.
+ * csa2_pages_resize: seq[i] gets new_len[i] entries: 0 frees it, fewer
+ *   releases the pages behind, more takes pages for what is to be appended
+ *   (their rows are as they were). When it keeps a partial last page that
+ *   other sequences hold too (counted before the call), that page is replaced
+ *   by a copy of its own, so that appends stay private.
+ * csa2_pages_compact: with L live pages, the live pages at L and above move
+ *   into the free ones below L, both in ascending order; refs and the rows of
+ *   all sequences follow. move_src, move_dst [rows_cap / page_size / 2] get
+ *   the moves, then -1 (for csa2_pages_copy on further caches); n_live (may be
+ *   NULL) gets L.
+ * The cached window rows (swa) are not paged: a forked sequence's ring is
+ * copied by the caller.
+ * refs, tables and lengths must be consistent; a table entry outside the
+ * cache sets CSA2_DEVERR_BAD_ROW and is treated as no page.
+ * n = 0 is a no-op. ws: csa2_pages_workspace_size(n, batch, rows_cap /
+ * page_size) bytes, n = 0 for csa2_pages_compact; csa2_pages_copy needs none.
+ */
+csa2_status csa2_pages_copy(const csa2_kv_desc *kv, const int32_t *src, const int32_t *dst, int32_t n,
+                            cudaStream_t stream);
+csa2_status csa2_pages_fork(const csa2_kv_desc *kv, int32_t *refs, const int32_t *parent, const int32_t *child,
+                            const int32_t *length, int32_t n, int32_t *copy_src, int32_t *copy_dst, void *ws,
+                            size_t ws_bytes, cudaStream_t stream);
+csa2_status csa2_pages_resize(const csa2_kv_desc *kv, int32_t *refs, const int32_t *seq, const int32_t *new_len,
+                              int32_t n, int32_t *copy_src, int32_t *copy_dst, void *ws, size_t ws_bytes,
+                              cudaStream_t stream);
+csa2_status csa2_pages_compact(const csa2_kv_desc *kv, int32_t *refs, int32_t *move_src, int32_t *move_dst,
+                               int32_t *n_live, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t csa2_pages_workspace_size(int32_t n, int32_t batch, int64_t num_pages);
+
+/*
+ * Decode attention of sequences that share a prefix, the prefix read and
+ * dequantised once for all of them (no counterpart in the pages: the dense
+ * form of csa2_sparse_attn_decode, for batches forked from one prompt).
+ *   members [n_members]: sequence ids; group g is members[group_begin[g]] up
+ *   to members[group_begin[g + 1] - 1] (group_begin [n_groups + 1]). Group
+ *   g's entries below prefix_len[g] are read through the page-table row of
+ *   its first member, entries from there on through each sequence's own row.
+ *   With equal prefixes (csa2_pages_fork makes them) that is attention over
+ *   every entry of each sequence. A sequence alone is a group of one.
+ *   q_bf16 [nq][h][d], query i of sequence i / q_per_seq, sees the entries
+ *   below q_limit[i] (q_limit NULL: seq_len of its sequence) and its window
+ *   rows (swa, swa_seq_stride, swa_begin, swa_end, w_max as in
+ *   csa2_sparse_attn_decode):
+ *     o_h = sum_j softmax_j(softmax_scale * <q_h, v_j>) v_j
+ *   written as bf16 o [nq][h][d] and lse [nq][h] (nullable). A query that
+ *   sees nothing gets o = 0, lse = -inf; o and lse of sequences in no group
+ *   stay as they were. h in 1 ... CSA2_PREFIX_MAX_HEADS.
+ * An entry outside the page table or the cache is left out and sets
+ * CSA2_DEVERR_BAD_ROW, and so do a member outside the batch (skipped), a
+ * group that does not lie within members (skipped) and a bad window
+ * (dropped). A sequence is to be listed once: o of one listed twice may be
+ * that of either place. Arithmetic and the range of q are those of
+ * csa2_sparse_attn_decode. n_groups = 0 is a no-op.
+ * ws: at least csa2_prefix_attn_workspace_size(n_members, n_groups,
+ * q_per_seq, h) bytes, whatever the lengths.
+ */
+#define CSA2_PREFIX_MAX_HEADS 128
+csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_per_seq, int32_t h,
+                                    const csa2_kv_desc *kv, const int32_t *members, int32_t n_members,
+                                    const int32_t *group_begin, const int32_t *prefix_len, int32_t n_groups,
+                                    const int32_t *q_limit, const uint8_t *swa, int64_t swa_seq_stride,
+                                    const int32_t *swa_begin, const int32_t *swa_end, int32_t w_max,
+                                    float softmax_scale, void *o_bf16, float *lse, void *ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+size_t csa2_prefix_attn_workspace_size(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h);
+
+/*
  * Building blocks of a long sequence decoded with its entries split across
  * GPUs by entry range (one exchange step per layer; the pages put 1M-token
  * contexts on one sequence: [P3] "CSA2 tackles storage", [P4] "How does the
@@ -346,6 +449,7 @@ csa2_status csa2_attn_merge(const float *o_parts, const float *lse_parts, int32_
 #define CSA2_DEVERR_WAIT_TIMEOUT 2u  /* a bounded barrier wait gave up         */
 #define CSA2_DEVERR_SELECT 4u        /* selection produced more ids than asked  */
 #define CSA2_DEVERR_Q_RANGE 8u       /* attention q outside f16's finite range  */
+#define CSA2_DEVERR_PAGES 16u        /* a page operator refused an entry        */
 csa2_status csa2_device_status(cudaStream_t stream, uint32_t *code);
 
 /*

@@ -67,6 +67,14 @@ _SIGS = {
     "csa2_sparse_attn_nvfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
     "csa2_sparse_attn_decode_static": (_i32, [_vp, _i32, _i32, _i32, _kvp, _vp, _i32, _vp, _i64, _vp, _vp, _i32,
                                               _f32, _vp, _vp, _vp]),
+    "csa2_pages_copy": (_i32, [_kvp, _vp, _vp, _i32, _vp]),
+    "csa2_pages_fork": (_i32, [_kvp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "csa2_pages_resize": (_i32, [_kvp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "csa2_pages_compact": (_i32, [_kvp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "csa2_pages_workspace_size": (_sz, [_i32, _i32, _i64]),
+    "csa2_prefix_attn_decode": (_i32, [_vp, _i32, _i32, _i32, _kvp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _vp,
+                                       _vp, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "csa2_prefix_attn_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
     "csa2_score_ids": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _kvp, _i32, _vp, _vp]),
     "csa2_select_keys": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "csa2_sparse_attn_partial": (_i32, [_vp, _i32, _i32, _i32, _kvp, _vp, _i32, _vp, _i64, _vp, _vp, _i32,
@@ -219,6 +227,53 @@ def csa2_append_kidx_e4m3(x_bf16, seq, pos, kv: KvCache, stream=None):
     """Indexer keys x [n][di] into the physical rows of (seq, pos) of the key array."""
     _check("csa2_append_kidx_e4m3", _lib.csa2_append_kidx_e4m3(
         _ptr(x_bf16), x_bf16.shape[0], _ptr(seq), _ptr(pos), kv.desc, _stream(stream)))
+
+
+def _bytes(ws):
+    return ws.numel() * ws.element_size() if ws is not None else 0
+
+
+def csa2_pages_workspace_size(n, batch, num_pages):
+    return _lib.csa2_pages_workspace_size(n, batch, num_pages)
+
+
+def csa2_pages_copy(kv: KvCache, src, dst, stream=None):
+    """Pages src[i] -> dst[i] (codes, scales, keys); -1 is an empty slot."""
+    _check("csa2_pages_copy", _lib.csa2_pages_copy(kv.desc, _ptr(src), _ptr(dst), src.shape[0], _stream(stream)))
+
+
+def csa2_pages_fork(kv: KvCache, refs, parent, child, length, copy_src, copy_dst, ws, stream=None):
+    """Empty sequences child[i] become the first length[i] entries (None: all) of parent[i], sharing whole pages."""
+    _check("csa2_pages_fork", _lib.csa2_pages_fork(
+        kv.desc, _ptr(refs), _ptr(parent), _ptr(child), _ptr(length), parent.shape[0], _ptr(copy_src), _ptr(copy_dst),
+        _ptr(ws), _bytes(ws), _stream(stream)))
+
+
+def csa2_pages_resize(kv: KvCache, refs, seq, new_len, copy_src, copy_dst, ws, stream=None):
+    """seq[i] gets new_len[i] entries: pages are released or taken, 0 frees the sequence."""
+    _check("csa2_pages_resize", _lib.csa2_pages_resize(
+        kv.desc, _ptr(refs), _ptr(seq), _ptr(new_len), seq.shape[0], _ptr(copy_src), _ptr(copy_dst), _ptr(ws),
+        _bytes(ws), _stream(stream)))
+
+
+def csa2_pages_compact(kv: KvCache, refs, move_src, move_dst, n_live, ws, stream=None):
+    """Live pages move into the lowest page numbers; the moves go to move_src / move_dst (then -1)."""
+    _check("csa2_pages_compact", _lib.csa2_pages_compact(
+        kv.desc, _ptr(refs), _ptr(move_src), _ptr(move_dst), _ptr(n_live), _ptr(ws), _bytes(ws), _stream(stream)))
+
+
+def csa2_prefix_attn_workspace_size(n_members, n_groups, q_per_seq, h):
+    return _lib.csa2_prefix_attn_workspace_size(n_members, n_groups, q_per_seq, h)
+
+
+def csa2_prefix_attn_decode(q_bf16, q_per_seq, kv: KvCache, members, group_begin, prefix_len, q_limit, swa, swa_seq_stride,
+                            swa_begin, swa_end, w_max, softmax_scale, o_bf16, lse, ws, stream=None):
+    """Attention over whole sequences and their windows, each group's first prefix_len entries read once for all of it."""
+    nq, h = q_bf16.shape[0], q_bf16.shape[1]
+    _check("csa2_prefix_attn_decode", _lib.csa2_prefix_attn_decode(
+        _ptr(q_bf16), nq, q_per_seq, h, kv.desc, _ptr(members), members.shape[0], _ptr(group_begin), _ptr(prefix_len),
+        prefix_len.shape[0], _ptr(q_limit), _ptr(swa), int(swa_seq_stride), _ptr(swa_begin), _ptr(swa_end), int(w_max),
+        float(softmax_scale), _ptr(o_bf16), _ptr(lse), _ptr(ws), _bytes(ws), _stream(stream)))
 
 
 def csa2_score_ids(qidx, w, q_per_seq, ids, kv: KvCache, id_offset, keys, stream=None):

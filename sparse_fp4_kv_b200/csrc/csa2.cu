@@ -24,6 +24,8 @@
 #include "indexer.cuh"
 #include "indexer_fused.cuh"
 #include "indexer_batch.cuh"
+#include "pages.cuh"
+#include "prefix_attn.cuh"
 
 using namespace csa2;
 
@@ -1387,3 +1389,213 @@ extern "C" csa2_status csa2_sparse_attn_decode_static(const void *q_bf16, int32_
                                    w_max, softmax_scale, o_bf16, lse, scratch, CSA2_ATTN_STATIC_SCRATCH_BYTES,
                                    stream);
 }
+
+// ---------------------------------------------------------------------------
+// Page operators and attention over shared prefixes
+// ---------------------------------------------------------------------------
+namespace {
+
+struct PagesLayout {
+    size_t off_entry, off_claim, off_fresh, total;
+};
+PagesLayout pages_layout(int32_t n, int32_t batch, int64_t num_pages) {
+    PagesLayout L{};
+    L.off_entry = 256;  // behind the head
+    L.off_claim = align_up(L.off_entry + (size_t)n * sizeof(PageEntry), 256);
+    L.off_fresh = align_up(L.off_claim + (size_t)batch * 4, 256);
+    L.total = align_up(L.off_fresh + (size_t)num_pages * 4, 256);
+    return L;
+}
+
+// Arguments that every page operator checks, and the parameters they set.
+csa2_status pages_setup(const csa2_kv_desc *kv, PagesParams &p) {
+    const csa2_status st = check_kv(kv, kv && kv->kidx);
+    if (st != CSA2_OK) return st;
+    const int64_t pages = kv->rows_cap / kv->page_size;
+    if (pages <= 0) return CSA2_ERR_INVALID_ARG;
+    p.kv = *kv;
+    p.num_pages = (int32_t)pages;
+    // the descriptor's tables are read-only for every other call
+    p.table = const_cast<int32_t *>(kv->page_table);
+    p.seq_len = const_cast<int32_t *>(kv->seq_len);
+    return CSA2_OK;
+}
+
+csa2_status pages_workspace(PagesParams &p, void *ws, size_t ws_bytes) {
+    const PagesLayout L = pages_layout(p.n, p.kv.batch, p.num_pages);
+    if (!ws || ws_bytes < L.total || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    p.head = reinterpret_cast<int32_t *>(b);
+    p.entry = reinterpret_cast<PageEntry *>(b + L.off_entry);
+    p.claim = reinterpret_cast<int32_t *>(b + L.off_claim);
+    p.fresh = reinterpret_cast<int32_t *>(b + L.off_fresh);
+    return CSA2_OK;
+}
+
+// Blocks for a copy of up to `rows` rows: a warp per unit, at most one wave
+// of full SMs (the warps stride over what is left).
+unsigned copy_blocks(int64_t rows) {
+    const int64_t units = rows / kCopyUnitRows, warps = kApplyThreads / 32;
+    const int64_t wave = (int64_t)num_sms() * (2048 / kApplyThreads);
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(wave, (units + warps - 1) / warps));
+}
+
+template <bool FORK>
+csa2_status pages_run(PagesParams &p, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    const csa2_status st = pages_workspace(p, ws, ws_bytes);
+    if (st != CSA2_OK) return st;
+    launch_cluster(k_pages_plan<FORK>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream, kPlanCtas, p);
+    if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
+    // along x: enough blocks for the longest row at four columns a thread and
+    // for a page copy, but no more than fill the machine with all entries
+    const int64_t cols = ((int64_t)p.kv.max_pages + 4 * kApplyThreads - 1) / (4 * kApplyThreads);
+    const int64_t most = std::max<int64_t>(1, (int64_t)num_sms() * (2048 / kApplyThreads) / std::min(p.n, 65535));
+    const int64_t x = std::min(most, std::max<int64_t>(cols, copy_blocks(p.kv.page_size)));
+    launch(k_pages_apply<FORK>, dim3((unsigned)x, (unsigned)std::min(p.n, 65535)), dim3(kApplyThreads), 0, stream, p);
+    return check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t csa2_pages_workspace_size(int32_t n, int32_t batch, int64_t num_pages) {
+    if (n < 0 || batch <= 0 || num_pages <= 0 || num_pages > INT32_MAX) return 0;
+    return pages_layout(n, batch, num_pages).total;
+}
+
+csa2_status csa2_pages_copy(const csa2_kv_desc *kv, const int32_t *src, const int32_t *dst, int32_t n,
+                            cudaStream_t stream) {
+    PagesParams p{};
+    const csa2_status st = pages_setup(kv, p);
+    if (st != CSA2_OK) return st;
+    if (n < 0) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return CSA2_ERR_INVALID_ARG;
+    p.n = n;
+    p.copy_src = const_cast<int32_t *>(src);
+    p.copy_dst = const_cast<int32_t *>(dst);
+    launch(k_pages_copy, dim3(copy_blocks((int64_t)n * kv->page_size)), dim3(kApplyThreads), 0, stream, p);
+    return check_launch();
+}
+
+csa2_status csa2_pages_fork(const csa2_kv_desc *kv, int32_t *refs, const int32_t *parent, const int32_t *child,
+                            const int32_t *length, int32_t n, int32_t *copy_src, int32_t *copy_dst, void *ws,
+                            size_t ws_bytes, cudaStream_t stream) {
+    PagesParams p{};
+    const csa2_status st = pages_setup(kv, p);
+    if (st != CSA2_OK) return st;
+    if (n < 0) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (!refs || !parent || !child || !aligned(refs, 4) || !aligned(parent, 4) || !aligned(child, 4) ||
+        !aligned(length, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !copy_src != !copy_dst)
+        return CSA2_ERR_INVALID_ARG;
+    p.refs = refs;
+    p.n = n;
+    p.from = parent;
+    p.to = child;
+    p.length = length;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    return pages_run<true>(p, ws, ws_bytes, stream);
+}
+
+csa2_status csa2_pages_resize(const csa2_kv_desc *kv, int32_t *refs, const int32_t *seq, const int32_t *new_len,
+                              int32_t n, int32_t *copy_src, int32_t *copy_dst, void *ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+    PagesParams p{};
+    const csa2_status st = pages_setup(kv, p);
+    if (st != CSA2_OK) return st;
+    if (n < 0) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (!refs || !seq || !new_len || !aligned(refs, 4) || !aligned(seq, 4) || !aligned(new_len, 4) ||
+        !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !copy_src != !copy_dst)
+        return CSA2_ERR_INVALID_ARG;
+    p.refs = refs;
+    p.n = n;
+    p.to = seq;
+    p.length = new_len;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    return pages_run<false>(p, ws, ws_bytes, stream);
+}
+
+csa2_status csa2_pages_compact(const csa2_kv_desc *kv, int32_t *refs, int32_t *move_src, int32_t *move_dst,
+                               int32_t *n_live, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    PagesParams p{};
+    csa2_status st = pages_setup(kv, p);
+    if (st != CSA2_OK) return st;
+    if (!refs || !aligned(refs, 4) || !aligned(move_src, 4) || !aligned(move_dst, 4) || !aligned(n_live, 4))
+        return CSA2_ERR_INVALID_ARG;
+    if (p.num_pages > 1 && (!move_src || !move_dst)) return CSA2_ERR_INVALID_ARG;
+    p.refs = refs;
+    p.copy_src = move_src;
+    p.copy_dst = move_dst;
+    p.n_live = n_live;
+    if ((st = pages_workspace(p, ws, ws_bytes)) != CSA2_OK) return st;
+    launch_cluster(k_pages_compact_plan, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream, kPlanCtas, p);
+    if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
+    const int64_t rows = std::max<int64_t>((int64_t)(p.num_pages / 2) * kv->page_size, (int64_t)kv->batch * kv->max_pages / 4);
+    launch(k_pages_compact_apply, dim3(copy_blocks(rows)), dim3(kApplyThreads), 0, stream, p);
+    return check_launch();
+}
+
+size_t csa2_prefix_attn_workspace_size(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h) {
+    if (n_members <= 0 || n_groups <= 0 || q_per_seq <= 0 || h < 1 || h > CSA2_PREFIX_MAX_HEADS) return 0;
+    return 256;
+}
+
+csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_per_seq, int32_t h,
+                                    const csa2_kv_desc *kv, const int32_t *members, int32_t n_members,
+                                    const int32_t *group_begin, const int32_t *prefix_len, int32_t n_groups,
+                                    const int32_t *q_limit, const uint8_t *swa, int64_t swa_seq_stride,
+                                    const int32_t *swa_begin, const int32_t *swa_end, int32_t w_max,
+                                    float softmax_scale, void *o_bf16, float *lse, void *ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+    csa2_status st = check_kv(kv, false);
+    if (st != CSA2_OK) return st;
+    if (h < 1 || h > CSA2_PREFIX_MAX_HEADS) return CSA2_ERR_UNSUPPORTED;
+    if (nq <= 0 || nq > 65535 || q_per_seq <= 0 || (nq + q_per_seq - 1) / q_per_seq > kv->batch)
+        return CSA2_ERR_INVALID_ARG;
+    if (n_members < 0 || n_groups < 0 || n_members > kv->batch || n_groups > n_members) return CSA2_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale) || w_max < 0) return CSA2_ERR_INVALID_ARG;
+    if (n_groups == 0) return CSA2_OK;
+    if (!q_bf16 || !o_bf16 || !aligned(q_bf16, 16) || !aligned(o_bf16, 16) || !aligned(lse, 4)) return CSA2_ERR_INVALID_ARG;
+    if (!members || !group_begin || !prefix_len || !aligned(members, 4) || !aligned(group_begin, 4) ||
+        !aligned(prefix_len, 4) || !aligned(q_limit, 4))
+        return CSA2_ERR_INVALID_ARG;
+    const bool has_swa = swa_begin != nullptr;
+    if (has_swa && (!swa || !swa_end || swa_seq_stride <= 0 || !aligned(swa, 16) || !aligned(swa_begin, 4) || !aligned(swa_end, 4)))
+        return CSA2_ERR_INVALID_ARG;
+    if (!has_swa && w_max > 0) return CSA2_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < csa2_prefix_attn_workspace_size(n_members, n_groups, q_per_seq, h) || !aligned(ws, 256))
+        return CSA2_ERR_WORKSPACE;
+    PrefixParams p{};
+    p.q = static_cast<const uint16_t *>(q_bf16);
+    p.kv = *kv;
+    p.members = members;
+    p.group_begin = group_begin;
+    p.prefix_len = prefix_len;
+    p.q_limit = q_limit;
+    p.swa = has_swa ? swa : nullptr;
+    p.swa_seq_stride = swa_seq_stride;
+    p.swa_begin = swa_begin;
+    p.swa_end = has_swa ? swa_end : nullptr;
+    p.o = static_cast<uint16_t *>(o_bf16);
+    p.lse = lse;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.nq = nq;
+    p.q_per_seq = q_per_seq;
+    p.h = h;
+    p.w_max = w_max;
+    p.n_members = n_members;
+    p.n_groups = n_groups;
+    const size_t smem = (size_t)(kPsHeads + kPsTile) * CSA2_D * 4 + (size_t)kPsHeads * kPsTile * 4 + (3 * kPsHeads + kPsTile) * 4;
+    if (!smem_attr(k_prefix_attn_simple, smem)) return CSA2_ERR_CUDA;
+    const int64_t y = (int64_t)q_per_seq * ((h + kPsHeads - 1) / kPsHeads);
+    if (y > 65535) return CSA2_ERR_UNSUPPORTED;
+    launch(k_prefix_attn_simple, dim3((unsigned)n_members, (unsigned)y), dim3(kPsThreads), smem, stream, p);
+    return check_launch();
+}
+
+}  // extern "C"
