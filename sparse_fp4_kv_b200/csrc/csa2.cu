@@ -1440,6 +1440,66 @@ unsigned copy_blocks(int64_t rows) {
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>(wave, (units + warps - 1) / warps));
 }
 
+// Workspace of the attention over shared prefixes; nothing in it depends on
+// lengths. Partials: a pair of CTAs adds at most one to those of the strips.
+constexpr int64_t kPxMaxQueries = 1 << 17;
+struct PrefixLayout {
+    int32_t pairs, max_pre;
+    size_t off_start, off_mgroup, off_gstrip, off_gtiles, off_strips, off_pre_o, off_pre_lse, off_own_o, off_own_lse, total;
+};
+PrefixLayout prefix_layout(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h) {
+    PrefixLayout L{};
+    L.pairs = std::max(1, std::min(num_sms() / 2, kPxMergeParts / 2));
+    const int64_t n_own = (int64_t)n_members * q_per_seq;
+    L.max_pre = (int32_t)(n_own * h / kPxRows + n_groups);
+    size_t off = 256;  // the totals
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, 256);
+        return at;
+    };
+    L.off_start = take((size_t)L.pairs * 4);
+    L.off_mgroup = take((size_t)n_members * 4);
+    L.off_gstrip = take((size_t)n_groups * 4);
+    L.off_gtiles = take((size_t)n_groups * 8);
+    L.off_strips = take((size_t)(L.max_pre + n_own) * sizeof(PrefixStrip));
+    L.off_pre_o = take((size_t)(L.pairs + L.max_pre) * kPxRows * CSA2_D * 4);
+    L.off_pre_lse = take((size_t)(L.pairs + L.max_pre) * kPxRows * 4);
+    L.off_own_o = take((size_t)(L.pairs + n_own) * h * CSA2_D * 4);
+    L.off_own_lse = take((size_t)(L.pairs + n_own) * h * 4);
+    L.total = off;
+    return L;
+}
+
+// Pairs of CTAs of the attention kernel that the current device runs at once
+// (asked once per device, after its shared-memory attribute is set).
+int32_t prefix_resident_pairs() {
+    static std::mutex mu;
+    static std::map<int, int> per_dev;
+    const int dev = current_device();
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = per_dev.find(dev);
+    if (it != per_dev.end()) return it->second;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(kPxThreads);
+    cfg.dynamicSmemBytes = kPxSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_prefix_attn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    per_dev[dev] = n;
+    return n;
+}
+
 template <bool FORK>
 csa2_status pages_run(PagesParams &p, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const csa2_status st = pages_workspace(p, ws, ws_bytes);
@@ -1541,8 +1601,10 @@ csa2_status csa2_pages_compact(const csa2_kv_desc *kv, int32_t *refs, int32_t *m
 }
 
 size_t csa2_prefix_attn_workspace_size(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h) {
-    if (n_members <= 0 || n_groups <= 0 || q_per_seq <= 0 || h < 1 || h > CSA2_PREFIX_MAX_HEADS) return 0;
-    return 256;
+    if (n_members <= 0 || n_groups <= 0 || n_groups > n_members || q_per_seq <= 0 || h < 1 || h > CSA2_PREFIX_MAX_HEADS ||
+        (int64_t)n_members * q_per_seq > kPxMaxQueries)
+        return 0;
+    return prefix_layout(n_members, n_groups, q_per_seq, h).total;
 }
 
 csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_per_seq, int32_t h,
@@ -1557,7 +1619,9 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     if (h < 1 || h > CSA2_PREFIX_MAX_HEADS) return CSA2_ERR_UNSUPPORTED;
     if (nq <= 0 || nq > 65535 || q_per_seq <= 0 || (nq + q_per_seq - 1) / q_per_seq > kv->batch)
         return CSA2_ERR_INVALID_ARG;
-    if (n_members < 0 || n_groups < 0 || n_members > kv->batch || n_groups > n_members) return CSA2_ERR_INVALID_ARG;
+    if (n_members < 0 || n_groups < 0 || n_members > (nq + q_per_seq - 1) / q_per_seq || n_groups > n_members ||
+        (int64_t)n_members * q_per_seq > kPxMaxQueries)
+        return CSA2_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale) || w_max < 0) return CSA2_ERR_INVALID_ARG;
     if (n_groups == 0) return CSA2_OK;
     if (!q_bf16 || !o_bf16 || !aligned(q_bf16, 16) || !aligned(o_bf16, 16) || !aligned(lse, 4)) return CSA2_ERR_INVALID_ARG;
@@ -1568,8 +1632,8 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     if (has_swa && (!swa || !swa_end || swa_seq_stride <= 0 || !aligned(swa, 16) || !aligned(swa_begin, 4) || !aligned(swa_end, 4)))
         return CSA2_ERR_INVALID_ARG;
     if (!has_swa && w_max > 0) return CSA2_ERR_INVALID_ARG;
-    if (!ws || ws_bytes < csa2_prefix_attn_workspace_size(n_members, n_groups, q_per_seq, h) || !aligned(ws, 256))
-        return CSA2_ERR_WORKSPACE;
+    const PrefixLayout L = prefix_layout(n_members, n_groups, q_per_seq, h);
+    if (!ws || ws_bytes < L.total || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
     PrefixParams p{};
     p.q = static_cast<const uint16_t *>(q_bf16);
     p.kv = *kv;
@@ -1590,11 +1654,28 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     p.w_max = w_max;
     p.n_members = n_members;
     p.n_groups = n_groups;
-    const size_t smem = (size_t)(kPsHeads + kPsTile) * CSA2_D * 4 + (size_t)kPsHeads * kPsTile * 4 + (3 * kPsHeads + kPsTile) * 4;
-    if (!smem_attr(k_prefix_attn_simple, smem)) return CSA2_ERR_CUDA;
-    const int64_t y = (int64_t)q_per_seq * ((h + kPsHeads - 1) / kPsHeads);
-    if (y > 65535) return CSA2_ERR_UNSUPPORTED;
-    launch(k_prefix_attn_simple, dim3((unsigned)n_members, (unsigned)y), dim3(kPsThreads), smem, stream, p);
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    p.total_tiles = reinterpret_cast<int64_t *>(b);
+    p.n_pre = reinterpret_cast<int32_t *>(b + 8);
+    p.start = reinterpret_cast<int32_t *>(b + L.off_start);
+    p.member_group = reinterpret_cast<int32_t *>(b + L.off_mgroup);
+    p.group_strip = reinterpret_cast<int32_t *>(b + L.off_gstrip);
+    p.group_tiles = reinterpret_cast<int64_t *>(b + L.off_gtiles);
+    p.strips = reinterpret_cast<PrefixStrip *>(b + L.off_strips);
+    p.max_pre = L.max_pre;
+    p.pre_o = reinterpret_cast<float *>(b + L.off_pre_o);
+    p.pre_lse = reinterpret_cast<float *>(b + L.off_pre_lse);
+    p.own_o = reinterpret_cast<float *>(b + L.off_own_o);
+    p.own_lse = reinterpret_cast<float *>(b + L.off_own_lse);
+    if (!smem_attr(k_prefix_attn, kPxSmem)) return CSA2_ERR_CUDA;
+    // a second wave of pairs would double the time of equal runs
+    p.pairs = std::min(L.pairs, prefix_resident_pairs());
+    if (p.pairs < 1) return CSA2_ERR_CUDA;
+    launch(k_prefix_plan, dim3(1), dim3(kPxPlanThreads), 0, stream, p);
+    if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
+    launch(k_prefix_attn, dim3(2 * (unsigned)p.pairs), dim3(kPxThreads), kPxSmem, stream, p);
+    if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
+    launch(k_prefix_merge, dim3((unsigned)(n_members * q_per_seq), (unsigned)h), dim3(kPxMergeThreads), 0, stream, p);
     return check_launch();
 }
 

@@ -6,11 +6,54 @@
 //     o_h = sum_j softmax_j(scale * <q_h, v_j>) v_j
 // over the entries below the query's limit and its window rows (each row is
 // key and value, as in attn_decode.cuh).
+//
+// Bound. A prefix entry (288 bytes) meets every (query, head) row of its
+// group: 4 * 512 flops per row and entry, so from about 100 rows on the
+// tensor pipe bounds the prefix, not memory. The work is therefore cut by
+// rows, not by sequences: a strip is up to 128 rows of one group against the
+// group's prefix, or the heads of one query against its own rows (the entries
+// behind the prefix, then its window). A strip's rows of the cache are cut
+// into tiles of 256; all tiles form one list, and every pair of CTAs takes an
+// equal run of it. A run's part of a strip leaves an f32 partial (o divided
+// by its own denominator, and its log-sum-exp); k_prefix_merge joins a
+// query's partials of its prefix strip and of its own.
+//
+// Tile. A pair of CTAs (cta_group::2, M = 128: 64 rows of the strip each)
+// holds O [128][512] in f32 in both TMEMs: each CTA keeps its 64 rows, the
+// lanes 0..63 columns 0..255 and the lanes 64..127 columns 256..511. For S a
+// CTA holds the keys of half of the tile (128 of the N = 256 columns), for
+// P V all 256 rows of half of the latent width. One CTA alone could not:
+// O of 128 rows fills its TMEM, and of 64 rows costs the tensor pipe as much
+// as 128. N = 256 for both products, because with M = 128 per pair an
+// instruction takes 62 cycles at N = 128 and 64 at N = 256 (measured).
+// Shared memory: Q (64 KiB), P (32 KiB) and a ring of four 32 KiB chunks, in
+// the order the products take them: four chunks of 128 latent values of the
+// keys of tile i + 1, then up to four chunks of 64 rows of the values of
+// tile i, so that S of the next tile runs while the softmax of a tile does.
+//
+// Warps: 4 softmax warps (a thread has half a row: 128 scores), 8 that fetch
+// rows two chunks ahead into registers, dequantise them (exact in f16) and
+// store them swizzled, one that issues the products (in the first CTA).
 #pragma once
 
 #include "common.cuh"
 
 namespace csa2 {
+
+// One strip: rows of queries against a list of cache rows.
+struct __align__(16) PrefixStrip {
+    int64_t tile0;     // first tile in the call's list
+    int32_t ntiles;    // tiles of 256 rows (0: nothing to attend)
+    int32_t rows;      // length of the list of cache rows
+    int32_t seq;       // page-table row of its entries
+    int32_t t_base;    // id of the first entry
+    int32_t entries;   // FP4 entries of the list; the rest are window rows
+    int32_t w_begin;   // ring slot of the first window row
+    int32_t q_rows;    // rows of queries, at most 128
+    int32_t member0;   // prefix: first member of the group; own: -1
+    int32_t row0;      // prefix: first row among the group's (member, query, head) rows; own: query * h
+    int32_t w_seq;     // sequence of the window
+};
 
 struct PrefixParams {
     const uint16_t *q;  // bf16 [nq][h][512]
@@ -23,143 +66,862 @@ struct PrefixParams {
     uint16_t *o;
     float *lse;        // nullable
     float scale_log2;  // softmax scale * log2(e)
-    int32_t nq, q_per_seq, h, w_max, n_members, n_groups;
+    int32_t nq, q_per_seq, h, w_max, n_members, n_groups, pairs;
+    // workspace
+    int64_t *total_tiles;   // [1]
+    int32_t *n_pre;         // [1] prefix strips
+    int32_t *start;         // [pairs] first strip of each pair's run
+    int32_t *member_group;  // [n_members], -1: not computed
+    int32_t *group_strip;   // [n_groups] first strip of a group
+    int64_t *group_tiles;   // [n_groups] tiles of one strip of a group
+    PrefixStrip *strips;    // [max_pre + n_members * q_per_seq], the prefix strips first
+    int32_t max_pre;
+    float *pre_o, *pre_lse;  // [pairs + max_pre][128][512], [..][128]
+    float *own_o, *own_lse;  // [pairs + n_members * q_per_seq][h][512], [..][h]
 };
 
-constexpr int kPsThreads = 256;
-constexpr int kPsTile = 16;   // rows of a tile
-constexpr int kPsHeads = 16;  // heads of a block
+constexpr int kPxTile = 256;  // cache rows of a tile
+constexpr int kPxRows = 128;  // query rows of a strip
+constexpr int kPxSoftWarps = 4;
+constexpr int kPxLoadWarps = 8;
+constexpr int kPxMmaWarp = kPxSoftWarps + kPxLoadWarps;
+constexpr int kPxThreads = (kPxMmaWarp + 1) * 32;
+constexpr int kPxSlots = 4;
+constexpr int kPxSlotBytes = 32768;
+constexpr int kPxQBytes = 64 * CSA2_D * 2;
+constexpr int kPxPBytes = 64 * kPxTile * 2;
+constexpr int kPxMisc = 2048;
+constexpr size_t kPxSmem = 1024 + kPxQBytes + kPxPBytes + (size_t)kPxSlots * kPxSlotBytes + kPxMisc;
+constexpr float kPxRescale = 8.0f;  // log2 by which the maximum may rise before O is rescaled
+static_assert(kPxSmem <= 232448, "shared memory of one CTA");
 
-// One block per (member, query of the member, 16 heads); rows are staged as
-// f32, a warp takes two heads' scores and statistics, a thread two columns of
-// all 16 heads' outputs.
-__global__ void __launch_bounds__(kPsThreads) k_prefix_attn_simple(PrefixParams p) {
-    extern __shared__ float ps_smem[];
-    float *qs = ps_smem;                       // [16][512]
-    float *vs = qs + kPsHeads * CSA2_D;        // [kPsTile][512]
-    float *sc = vs + kPsTile * CSA2_D;         // [16][kPsTile] scores, then probabilities
-    float *mx = sc + kPsHeads * kPsTile;       // [16]
-    float *al = mx + kPsHeads;                 // [16]
-    float *ls = al + kPsHeads;                 // [16]
-    int32_t *bad = reinterpret_cast<int32_t *>(ls + kPsHeads);  // [kPsTile]
+// ---------------------------------------------------------------------------
+// cta_group::2 forms and cluster-scope barriers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc2(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on the same barrier of both CTAs when the products issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, "
+        "0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// mbar_wait with cluster scope (same limit and error).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    for (uint32_t n = 0; n < kWaitMaxPolls && global_ns() - t0 < kWaitNs; ++n) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        __nanosleep(64);
+    }
+    set_error(CSA2_DEVERR_WAIT_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------------------
+// the split of the tile list over the pairs: no more pairs than tiles, so that
+// every run has a tile and a strip's partials are those of consecutive pairs
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t total) { return (int32_t)min((int64_t)pairs, total); }
+__device__ __forceinline__ int64_t px_lo(int64_t total, int32_t pairs, int64_t c) { return c * total / pairs; }
+// the pair whose run holds tile x
+__device__ __forceinline__ int32_t px_owner(int64_t total, int32_t pairs, int64_t x) {
+    return (int32_t)(((x + 1) * pairs - 1) / total);
+}
+
+// Visible entries of query u of sequence s.
+__device__ __forceinline__ int32_t px_limit(const PrefixParams &p, int32_t s, int64_t u) {
+    const int64_t room = (int64_t)p.kv.max_pages * p.kv.page_size;
+    const int32_t n = p.q_limit ? p.q_limit[u] : p.kv.seq_len[s];
+    if (n > room) set_error(CSA2_DEVERR_BAD_ROW);
+    return (int32_t)min((int64_t)max(n, 0), room);
+}
+
+// ---------------------------------------------------------------------------
+// plan: one block lists the strips
+// ---------------------------------------------------------------------------
+constexpr int kPxPlanThreads = 1024;
+
+__device__ __forceinline__ int64_t px_block_exclusive(int64_t v, int64_t *warp_sums, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += u;
+        }
+        warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const int64_t before = (warp ? warp_sums[warp - 1] : 0) + s - v;
+    total = warp_sums[31];
+    __syncthreads();
+    return before;
+}
+
+__global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) {
+    __shared__ int64_t sums[32];
+    __shared__ int32_t descends;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    const int hc = (p.h + kPsHeads - 1) / kPsHeads;
-    const int32_t j = blockIdx.x, qi = blockIdx.y / hc, h0 = (blockIdx.y % hc) * kPsHeads;
-    const int32_t seq = p.members[j];
-    int32_t g = -1;
-    for (int32_t x = 0; x < p.n_groups; ++x)
-        if (p.group_begin[x] <= j && j < p.group_begin[x + 1]) g = x;
-    const int64_t u = (int64_t)seq * p.q_per_seq + qi;
-    if (seq < 0 || seq >= p.kv.batch || g < 0 || p.group_begin[g] < 0 || p.group_begin[g + 1] > p.n_members) {
-        if (tid == 0) set_error(CSA2_DEVERR_BAD_ROW);
-        return;
-    }
-    if (u >= p.nq) return;
-    const int32_t first = p.members[p.group_begin[g]];
-    const int32_t prefix = max(0, p.prefix_len[g]);
-    const int64_t limit = max(0, p.q_limit ? p.q_limit[u] : p.kv.seq_len[seq]);
-    int32_t wb = p.swa_begin ? p.swa_begin[u] : 0, nw = p.swa_begin ? max(0, p.swa_end[u] - wb) : 0;
-    if (nw > 0 && (wb < 0 || wb >= p.swa_seq_stride || nw > p.swa_seq_stride || nw > p.w_max)) {
-        if (tid == 0) set_error(CSA2_DEVERR_BAD_ROW);
-        nw = 0;
-    }
-    for (int i = tid; i < kPsHeads * CSA2_D; i += kPsThreads) {
-        const int hh = h0 + i / CSA2_D;
-        qs[i] = hh < p.h ? __uint_as_float((uint32_t)p.q[(u * p.h + hh) * CSA2_D + i % CSA2_D] << 16) * p.scale_log2 : 0.0f;
-    }
-    if (tid < kPsHeads) mx[tid] = -INFINITY, ls[tid] = 0.0f;
-    float acc[kPsHeads][2];
-#pragma unroll
-    for (int h = 0; h < kPsHeads; ++h) acc[h][0] = acc[h][1] = 0.0f;
-    const int64_t rows = limit + nw;
-    for (int64_t r0 = 0; r0 < rows; r0 += kPsTile) {
-        __syncthreads();
-        for (int i = tid; i < kPsTile * (CSA2_D / 16); i += kPsThreads) {
-            const int e = i / (CSA2_D / 16), blk = i % (CSA2_D / 16);
-            const int64_t r = r0 + e;
-            float *dst = vs + e * CSA2_D + blk * 16;
-            int ok = 0;
-            if (r < limit) {
-                const int32_t holder = r < prefix ? first : seq;
-                const int64_t row = holder >= 0 && holder < p.kv.batch ? physical_row(p.kv, holder, r) : -1;
-                if (row >= 0) {
-                    ok = 1;
-                    const uint2 c = *reinterpret_cast<const uint2 *>(p.kv.codes + row * (CSA2_D / 2) + blk * 8);
-                    const uint32_t sb = p.kv.scales[row * (CSA2_D / CSA2_BLOCK) + blk];
-                    const float s = e4m3x2_to_float2((uint16_t)sb).x;
-                    uint32_t h2[8];
-                    e2m1x8_to_f16x8(c.x, *reinterpret_cast<uint32_t(*)[4]>(h2));
-                    e2m1x8_to_f16x8(c.y, *reinterpret_cast<uint32_t(*)[4]>(h2 + 4));
-                    for (int t = 0; t < 8; ++t) {
-                        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(h2 + t));
-                        dst[2 * t] = f.x * s, dst[2 * t + 1] = f.y * s;
-                    }
-                } else {
+    if (tid == 0) descends = 0;
+    __syncthreads();
+    const int32_t n_own = p.n_members * p.q_per_seq, ps_rows = p.q_per_seq * p.h;
+    for (int32_t g = tid; g < p.n_groups; g += kPxPlanThreads)
+        if (p.group_begin[g] > p.group_begin[g + 1]) descends = 1;
+    for (int32_t j = tid; j < p.n_members; j += kPxPlanThreads) p.member_group[j] = -1;
+    for (int32_t c = tid; c < p.pairs; c += kPxPlanThreads) p.start[c] = 0;
+    __syncthreads();
+    // groups that overlap could not be told apart: a list that descends is refused as a whole
+    const bool all_bad = descends != 0;
+    if (all_bad && tid == 0) set_error(CSA2_DEVERR_BAD_ROW);
+    PrefixStrip *own = p.strips + p.max_pre;
+    for (int32_t i = tid; i < n_own; i += kPxPlanThreads) own[i].ntiles = 0;
+    __syncthreads();
+    // a warp per group: its members' lists, and how much of the prefix they see
+    for (int32_t g = warp; g < p.n_groups; g += kPxPlanThreads / 32) {
+        const int32_t b0 = p.group_begin[g], b1 = p.group_begin[g + 1];
+        const bool bad = all_bad || b0 < 0 || b1 > p.n_members;
+        int32_t seen = 0;
+        const int32_t prefix = max(0, p.prefix_len[g]);
+        const int32_t head = bad || b0 >= b1 ? -1 : p.members[b0];
+        if (!bad) {
+            for (int32_t i = b0 * p.q_per_seq + lane; i < b1 * p.q_per_seq; i += 32) {
+                const int32_t j = i / p.q_per_seq, qi = i - j * p.q_per_seq;
+                const int32_t s = p.members[j];
+                const int64_t u = (int64_t)s * p.q_per_seq + qi;
+                if (s < 0 || s >= p.kv.batch) {
                     set_error(CSA2_DEVERR_BAD_ROW);
+                    continue;
                 }
-            } else if (r < rows) {
-                ok = 1;
-                const int64_t sl = (wb + (r - limit)) % p.swa_seq_stride;
-                const uint8_t *w = p.swa + ((int64_t)seq * p.swa_seq_stride + sl) * CSA2_D + blk * 16;
-                for (int t = 0; t < 16; ++t) dst[t] = e4m3x2_to_float2((uint16_t)w[t]).x;
+                p.member_group[j] = g;
+                if (u >= p.nq) continue;
+                const int32_t limit = px_limit(p, s, u);
+                seen = max(seen, min(limit, prefix));
+                int32_t wb = 0, nw = 0;
+                if (p.swa_begin) {
+                    wb = p.swa_begin[u];
+                    nw = max(0, p.swa_end[u] - wb);
+                    if (nw > 0 && (wb < 0 || wb >= p.swa_seq_stride || nw > p.swa_seq_stride || nw > p.w_max)) {
+                        set_error(CSA2_DEVERR_BAD_ROW);
+                        nw = 0;
+                    }
+                }
+                PrefixStrip t;
+                t.tile0 = 0;
+                t.entries = max(0, limit - prefix);
+                t.rows = t.entries + nw;
+                t.ntiles = (int32_t)(((int64_t)t.rows + kPxTile - 1) / kPxTile);
+                t.seq = s;
+                t.t_base = prefix;
+                t.w_begin = wb;
+                t.q_rows = p.h;
+                t.member0 = -1;
+                t.row0 = (int32_t)u * p.h;
+                t.w_seq = s;
+                own[i] = t;
             }
-            if (!ok)
-                for (int t = 0; t < 16; ++t) dst[t] = 0.0f;
-            if (blk == 0) bad[e] = !ok;
+        } else if (lane == 0) {
+            set_error(CSA2_DEVERR_BAD_ROW);
         }
-        __syncthreads();
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int h = warp * 2 + hh;
-            float top = -INFINITY;
-            for (int e = 0; e < kPsTile; ++e) {
-                float d = 0.0f;
-                for (int c = lane; c < CSA2_D; c += 32) d = fmaf(qs[h * CSA2_D + c], vs[e * CSA2_D + c], d);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-                if (bad[e]) d = -INFINITY;
-                if (lane == e) sc[h * kPsTile + e] = d;
-                top = fmaxf(top, d);
-            }
-            __syncwarp();
-            const float mo = mx[h], mn = fmaxf(mo, top);
-            const float at = mn == -INFINITY ? 0.0f : mn;
-            float pr = lane < kPsTile ? exp2f(sc[h * kPsTile + lane] - at) : 0.0f;
-            if (lane < kPsTile) sc[h * kPsTile + lane] = pr;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) pr += __shfl_xor_sync(0xFFFFFFFFu, pr, o);
-            __syncwarp();
-            if (lane == 0) {
-                al[h] = exp2f(mo - at);
-                ls[h] = ls[h] * al[h] + pr;
-                mx[h] = mn;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < kPsHeads; ++h) {
-            acc[h][0] *= al[h], acc[h][1] *= al[h];
-#pragma unroll
-            for (int e = 0; e < kPsTile; ++e) {
-                const float pr = sc[h * kPsTile + e];
-                acc[h][0] = fmaf(pr, vs[e * CSA2_D + tid], acc[h][0]);
-                acc[h][1] = fmaf(pr, vs[e * CSA2_D + tid + kPsThreads], acc[h][1]);
-            }
-        }
+        for (int o = 16; o; o >>= 1) seen = max(seen, __shfl_xor_sync(0xFFFFFFFFu, seen, o));
+        if (lane == 0) p.group_tiles[g] = head < 0 || head >= p.kv.batch ? 0 : ((int64_t)seen << 32) | (uint32_t)((seen + kPxTile - 1) / kPxTile);
     }
     __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kPsHeads; ++h) {
-        if (h0 + h >= p.h) break;
-        const float inv = ls[h] > 0.0f ? 1.0f / ls[h] : 0.0f;
-        uint16_t *dst = p.o + (u * p.h + h0 + h) * CSA2_D;
-        dst[tid] = f32_to_bf16_bits(acc[h][0] * inv);
-        dst[tid + kPsThreads] = f32_to_bf16_bits(acc[h][1] * inv);
-        if (tid == 0 && p.lse)
-            p.lse[u * p.h + h0 + h] = ls[h] > 0.0f ? (mx[h] + log2f(ls[h])) * 0.69314718055994531f : -INFINITY;
+    // prefix strips: where each group's start, and their tiles
+    int64_t strips = 0, tiles = 0;
+    for (int32_t g0 = 0; g0 < p.n_groups; g0 += kPxPlanThreads) {
+        const int32_t g = g0 + tid;
+        int32_t n = 0, nt = 0, seen = 0, b0 = 0, rows = 0;
+        if (g < p.n_groups && p.group_tiles[g] != 0) {
+            b0 = p.group_begin[g];
+            rows = (p.group_begin[g + 1] - b0) * ps_rows;
+            n = (rows + kPxRows - 1) / kPxRows;
+            nt = (int32_t)(p.group_tiles[g] & 0xFFFFFFFF);
+            seen = (int32_t)(p.group_tiles[g] >> 32);
+        }
+        int64_t ts, tt;
+        const int64_t s0 = strips + px_block_exclusive(n, sums, ts);
+        const int64_t t0 = tiles + px_block_exclusive((int64_t)n * nt, sums, tt);
+        if (g < p.n_groups) p.group_strip[g] = n ? (int32_t)s0 : -1;
+        for (int32_t x = 0; x < n && s0 + x < p.max_pre; ++x) {
+            PrefixStrip t;
+            t.tile0 = t0 + (int64_t)x * nt;
+            t.ntiles = nt;
+            t.rows = seen;
+            t.seq = p.members[b0];
+            t.t_base = 0;
+            t.entries = seen;
+            t.w_begin = 0;
+            t.q_rows = min(kPxRows, rows - x * kPxRows);
+            t.member0 = b0;
+            t.row0 = x * kPxRows;
+            t.w_seq = 0;
+            p.strips[s0 + x] = t;
+        }
+        strips += ts;
+        tiles += tt;
     }
+    const int32_t n_pre = (int32_t)strips;
+    for (int32_t i0 = 0; i0 < n_own; i0 += kPxPlanThreads) {
+        const int32_t i = i0 + tid;
+        int64_t tt;
+        const int64_t t0 = tiles + px_block_exclusive(i < n_own ? own[i].ntiles : 0, sums, tt);
+        if (i < n_own) own[i].tile0 = t0;
+        tiles += tt;
+    }
+    if (tid == 0) {
+        *p.total_tiles = tiles;
+        *p.n_pre = n_pre;
+    }
+    if (tiles == 0) return;
+    // the first strip of every pair's run
+    const int32_t pairs = px_pairs(p.pairs, tiles);
+    for (int32_t i = tid; i < n_pre + n_own; i += kPxPlanThreads) {
+        const PrefixStrip &t = i < n_pre ? p.strips[i] : own[i - n_pre];
+        if (t.ntiles == 0) continue;
+        // pairs c with tile0 <= lo(c) < tile0 + ntiles
+        const int64_t t1 = t.tile0 + t.ntiles;
+        for (int64_t c = (t.tile0 * pairs + tiles - 1) / tiles; c < pairs && px_lo(tiles, pairs, c) < t1; ++c)
+            p.start[c] = i;
+    }
+}
+
+// A role's walk over the tiles of a pair's run.
+struct PxWalk {
+    PrefixStrip t;
+    int32_t s, tile, n_pre;  // strip, tile within it
+    __device__ __forceinline__ void load(const PrefixParams &p) {
+        t = s < n_pre ? p.strips[s] : p.strips[p.max_pre + (s - n_pre)];
+    }
+    __device__ __forceinline__ void begin(const PrefixParams &p, int32_t c, int64_t x0) {
+        n_pre = *p.n_pre;
+        s = p.start[c];
+        load(p);
+        tile = (int32_t)(x0 - t.tile0);
+    }
+    __device__ __forceinline__ bool last() const { return tile == t.ntiles - 1; }
+    // only while tiles are left: strips without tiles are passed over
+    __device__ __forceinline__ void next(const PrefixParams &p) {
+        if (++tile < t.ntiles) return;
+        tile = 0;
+        do {
+            ++s;
+            load(p);
+        } while (t.ntiles == 0);
+    }
+    __device__ __forceinline__ int value_chunks() const { return (min(kPxTile, t.rows - tile * kPxTile) + 63) >> 6; }
+};
+
+// Where row r of the walk's tile lies: >= 0 a physical cache row, kPxNone no
+// row, else -2 - slot of the window ring.
+constexpr int32_t kPxNone = -1;
+__device__ __forceinline__ int32_t px_resolve(const PrefixParams &p, const PxWalk &w, int r) {
+    const int32_t j = w.tile * kPxTile + r;
+    if (j >= w.t.rows) return kPxNone;
+    if (j < w.t.entries) {
+        const int64_t row = physical_row(p.kv, w.t.seq, (int64_t)w.t.t_base + j);
+        if (row < 0) {
+            set_error(CSA2_DEVERR_BAD_ROW);
+            return kPxNone;
+        }
+        return (int32_t)row;
+    }
+    int64_t sl = (int64_t)w.t.w_begin + (j - w.t.entries);  // below twice the stride
+    if (sl >= p.swa_seq_stride) sl -= p.swa_seq_stride;
+    return -2 - (int32_t)sl;
+}
+
+// 64 values of a row: raw bytes as loaded.
+struct PxRaw {
+    uint4 v[4];
+    uint32_t sc;
+    int32_t src;
+};
+__device__ __forceinline__ void px_fetch(const PrefixParams &p, const uint8_t *swa_seq, int32_t src, int blk, PxRaw &raw) {
+    raw.src = src;
+    if (src >= 0) {
+        const uint4 *c = reinterpret_cast<const uint4 *>(p.kv.codes + (int64_t)src * (CSA2_D / 2) + blk * 32);
+        raw.v[0] = __ldg(c);
+        raw.v[1] = __ldg(c + 1);
+        raw.sc = __ldg(reinterpret_cast<const uint32_t *>(p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + blk * 4));
+    } else if (src != kPxNone) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(swa_seq + (int64_t)(-2 - src) * CSA2_D + blk * 64);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw.v[j] = __ldg(w + j);
+    }
+}
+// Dequantised into a 128-byte row of a swizzled block (dst: the row, r8: row & 7).
+__device__ __forceinline__ void px_store(const PxRaw &raw, uint8_t *dst, int r8) {
+    if (raw.src >= 0) {
+        const uint32_t w[8] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w, raw.v[1].x, raw.v[1].y, raw.v[1].z, raw.v[1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t sb = (raw.sc >> (8 * (j >> 1))) & 0xFFu;
+            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(sb | (sb << 8)));
+            uint32_t h[4];
+            e2m1x8_to_f16x8(w[j], h);
+            *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) =
+                make_uint4(hmul2_u32(h[0], s2), hmul2_u32(h[1], s2), hmul2_u32(h[2], s2), hmul2_u32(h[3], s2));
+        }
+    } else if (raw.src != kPxNone) {
+        const uint32_t w[16] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w, raw.v[1].x, raw.v[1].y, raw.v[1].z, raw.v[1].w,
+                                raw.v[2].x, raw.v[2].y, raw.v[2].z, raw.v[2].w, raw.v[3].x, raw.v[3].y, raw.v[3].z, raw.v[3].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) =
+                make_uint4(e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
+                           e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// Row of q (query * h + head) of row r of a strip and the entries it sees of
+// the strip's list; -1 where there is none.
+__device__ __forceinline__ int32_t px_q_row(const PrefixParams &p, const PrefixStrip &t, int r, int32_t &sees) {
+    sees = 0;
+    if (r >= t.q_rows) return -1;
+    if (t.member0 < 0) {
+        sees = t.rows;
+        return t.row0 + r;
+    }
+    const int32_t x = t.row0 + r, per = p.q_per_seq * p.h;
+    const int32_t j = x / per, y = x - j * per;
+    const int32_t s = p.members[t.member0 + j];
+    if (s < 0 || s >= p.kv.batch) return -1;
+    const int64_t u = (int64_t)s * p.q_per_seq + y / p.h;
+    if (u >= p.nq) return -1;
+    sees = min(px_limit(p, s, u), t.rows);
+    return (int32_t)u * p.h + y % p.h;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_prefix_attn(PrefixParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *q_s = base;                         // [8 blocks of 64 values][64 rows][128 B]
+    uint8_t *p_s = q_s + kPxQBytes;              // [4 blocks of 64 cache rows][64 rows][128 B]
+    uint8_t *ring = p_s + kPxPBytes;             // [kPxSlots][32 KiB]
+    uint8_t *misc = ring + kPxSlots * kPxSlotBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots] (first CTA's: both CTAs' loaders arrive)
+    uint64_t *empty = full + kPxSlots;                    // [kPxSlots]
+    uint64_t *s_full = empty + kPxSlots;                  // [2]
+    uint64_t *pv_done = s_full + 2;
+    uint64_t *p_full = pv_done + 1;  // (first CTA's)
+    uint64_t *q_full = p_full + 1;   // (first CTA's)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 1);
+    uint32_t *valid = tmem_slot + 2;                            // [4 tiles][8 words] resolved rows
+    float *xch = reinterpret_cast<float *>(valid + 32);         // [3][128] maxima of even and odd tiles, sums
+    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 384);   // [64]
+    static_assert(8 * (2 * kPxSlots + 5) + 8 + 128 + 1536 + 256 <= kPxMisc, "misc");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    pdl_trigger();
+    if (warp == 0) {
+        tmem_alloc2(tmem_slot, 512);
+        tmem_relinquish2();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kPxSlots; ++i) {
+            mbar_init(&full[i], 2 * kPxLoadWarps);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(pv_done, 1);
+        mbar_init(p_full, 2 * kPxSoftWarps);
+        mbar_init(q_full, 2 * kPxSoftWarps);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are initialised, both TMEMs allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    const int32_t c = blockIdx.x >> 1;
+    const int64_t total = *p.total_tiles;
+    const int32_t pairs = px_pairs(p.pairs, total);
+    const int64_t x0 = c < pairs ? px_lo(total, pairs, c) : 0;
+    const int n = c < pairs ? (int)(px_lo(total, pairs, c + 1) - x0) : 0;
+    constexpr uint32_t kColS = 256;
+
+    if (n > 0 && warp == kPxMmaWarp) {
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc_s = idesc_f16_f32(128, 256, 0, 0), idesc_o = idesc_f16_f32(128, 256, 0, 1);
+            const uint64_t a_q = make_sdesc(smem_u32(q_s), 16, 1024, kSw128);
+            const uint64_t a_p = make_sdesc(smem_u32(p_s), 16, 1024, kSw128);
+            const uint64_t b_k = make_sdesc(smem_u32(ring), 16, 1024, kSw128);
+            const uint64_t b_v = make_sdesc(smem_u32(ring), 8192, 1024, kSw128);
+            PxWalk wk, wv;  // tiles of S and of P V
+            wk.begin(p, c, x0);
+            wv = wk;
+            uint32_t chunk = 0, strips = 0;
+            bool ok = true;
+            auto scores = [&](int i) {
+                if (i == 0 || wk.tile == 0) ok = ok && mbar_wait_cluster(q_full, strips++ & 1u);
+                for (int d = 0; d < 4 && ok; ++d, ++chunk) {
+                    const uint32_t slot = chunk % kPxSlots;
+                    ok = mbar_wait_cluster(&full[slot], (chunk / kPxSlots) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // blocks of 64 values: two of the chunk
+                        mma_f16_pair(tmem + kColS + 128 * (i & 1), a_q + (uint64_t)(((2 * d + (k >> 2)) * 8192 + (k & 3) * 32) >> 4),
+                                     b_k + (uint64_t)((slot * kPxSlotBytes + (k >> 2) * 16384 + (k & 3) * 32) >> 4), idesc_s,
+                                     (d | k) ? 1u : 0u);
+                    tc_commit_pair(&empty[slot]);
+                }
+                if (ok) tc_commit_pair(&s_full[i & 1]);
+            };
+            scores(0);
+            for (int i = 0; i < n && ok; ++i) {
+                if (i + 1 < n) {
+                    wk.next(p);
+                    scores(i + 1);
+                }
+                ok = ok && mbar_wait_cluster(p_full, (uint32_t)i & 1u);
+                const bool fresh = i == 0 || wv.tile == 0;
+                const int nv = wv.value_chunks();
+                for (int d = 0; d < nv && ok; ++d, ++chunk) {
+                    const uint32_t slot = chunk % kPxSlots;
+                    ok = mbar_wait_cluster(&full[slot], (chunk / kPxSlots) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            mma_f16_pair(tmem + 128 * j, a_p + (uint64_t)((d * 8192 + k * 32) >> 4),
+                                         b_v + (uint64_t)((slot * kPxSlotBytes + j * 16384 + k * 2048) >> 4), idesc_o,
+                                         (!fresh || d > 0 || k > 0) ? 1u : 0u);
+                    tc_commit_pair(&empty[slot]);
+                }
+                if (ok) tc_commit_pair(pv_done);
+                if (i + 1 < n) wv.next(p);
+            }
+        }
+        __syncwarp();
+    } else if (n > 0 && warp >= kPxSoftWarps) {
+        // ---- rows of the cache into the ring ----
+        const int lw = warp - kPxSoftWarps;
+        const int k_row = 16 * lw + (lane & 15), k_blk = lane >> 4;         // keys: 16 rows x 2 blocks a warp
+        const int v_row = 8 * lw + (lane & 7), v_blk = 4 * rank + (lane >> 3);  // values: 8 rows x 4 blocks
+        uint32_t full_addr[kPxSlots];
+#pragma unroll
+        for (int i = 0; i < kPxSlots; ++i) full_addr[i] = cluster_smem_addr(&full[i], 0);
+        PxWalk w;
+        w.begin(p, c, x0);
+        // rows of a tile, resolved when its keys come up: the keys' one, the values' four
+        struct Rows {
+            int32_t k, v[4];
+            int nv;
+            const uint8_t *swa;
+        };
+        auto resolve = [&](int i) {
+            Rows r;
+            r.k = px_resolve(p, w, 128 * rank + k_row);
+            r.nv = w.value_chunks();
+            r.swa = p.swa ? p.swa + (int64_t)w.t.w_seq * p.swa_seq_stride * CSA2_D : nullptr;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                r.v[d] = px_resolve(p, w, 64 * d + v_row);
+                const uint32_t m = __ballot_sync(0xFFFFFFFFu, r.v[d] != kPxNone) & 0xFFu;
+                // rows 64 d + 8 lw .. + 7: a byte of word 2 d + lw / 4
+                if (lane == 0) reinterpret_cast<uint8_t *>(valid + (i & 3) * 8)[8 * d + lw] = (uint8_t)m;
+            }
+            return r;
+        };
+        uint32_t chunk = 0;
+        bool ok = true;
+        PxRaw raw[2];
+        auto fetch = [&](const Rows &r, bool keys, int d, PxRaw &x) {
+            if (keys) px_fetch(p, r.swa, r.k, 2 * d + k_blk, x);
+            else if (d < r.nv) px_fetch(p, r.swa, r.v[d], v_blk, x);
+        };
+        auto put = [&](const Rows &r, bool keys, int d, const PxRaw &x) {
+            if (!keys && d >= r.nv) return;
+            const uint32_t slot = chunk % kPxSlots, round = chunk / kPxSlots;
+            if (round > 0 && ok && !mbar_wait_cluster(&empty[slot], (round - 1) & 1u)) ok = false;
+            uint8_t *s = ring + slot * kPxSlotBytes;
+            if (ok) {
+                if (keys) px_store(x, s + k_blk * 16384 + k_row * 128, k_row & 7);
+                else px_store(x, s + (lane >> 3) * 8192 + v_row * 128, v_row & 7);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(slot == 0 ? full_addr[0] : slot == 1 ? full_addr[1] : slot == 2 ? full_addr[2] : full_addr[3]);
+            ++chunk;
+        };
+        // groups of four chunks: K(0), K(1), V(0), K(2), V(1), ...; the first two
+        // chunks of a group are fetched under the last two of the group before
+        auto group = [&](const Rows &r, bool keys, const Rows &rn, bool next_keys, bool has_next) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                put(r, keys, d, raw[d & 1]);
+                if (d < 2) fetch(r, keys, d + 2, raw[d & 1]);
+                else if (has_next) fetch(rn, next_keys, d - 2, raw[d & 1]);
+            }
+        };
+        Rows cur = resolve(0), nxt = cur;
+        fetch(cur, true, 0, raw[0]);
+        fetch(cur, true, 1, raw[1]);
+        if (n > 1) {
+            w.next(p);
+            nxt = resolve(1);
+        }
+        group(cur, true, n > 1 ? nxt : cur, n > 1, true);
+        if (n > 1) group(nxt, true, cur, false, true);
+        for (int i = 0; i < n && ok; ++i) {
+            // V(i), then K(i + 2)
+            Rows after = nxt;
+            if (i + 2 < n) {
+                w.next(p);
+                after = resolve(i + 2);
+                group(cur, false, after, true, true);
+                group(after, true, nxt, false, true);
+            } else {
+                group(cur, false, nxt, false, i + 1 < n);
+            }
+            cur = nxt;
+            nxt = after;
+        }
+    } else if (n > 0) {
+        // ---- softmax: this thread has row 64 * rank + (tid & 63) of a strip and half of its scores ----
+        const int r = tid & 63, half = tid >> 6;
+        const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t p_full_addr = cluster_smem_addr(p_full, 0), q_full_addr = cluster_smem_addr(q_full, 0);
+        const int pair_bar = 1 + (warp & 1);  // warps w and w + 2 have the same rows
+        PxWalk w;
+        w.begin(p, c, x0);
+        bool ok = true;
+        // Q of a strip into shared memory (f16): the barrier tells the products
+        auto load_q = [&](const PrefixStrip &t, int32_t &q_row, int32_t &sees) {
+            q_row = px_q_row(p, t, 64 * rank + r, sees);
+            if (half == 0) qrow_s[r] = q_row;
+            named_bar_sync(3, kPxSoftWarps * 32);
+            bool bad = false;
+            constexpr int kBatch = 8;
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32; k0 += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int32_t src = qrow_s[2 * (k0 + k) + half];
+                    v[k] = src >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)src * CSA2_D) + (tid & 63)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int row = 2 * (k0 + k) + half, c64 = tid & 63;
+                    const uint32_t w4[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    uint32_t o4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // 65536 and more (0x4780 and up, infinities and NaN too) have no finite f16 value
+                        bad |= (w4[j] & 0x7FFFu) >= 0x4780u || ((w4[j] >> 16) & 0x7FFFu) >= 0x4780u;
+                        const __half2 hh = __floats2half2_rn(__uint_as_float(w4[j] << 16), __uint_as_float(w4[j] & 0xFFFF0000u));
+                        o4[j] = *reinterpret_cast<const uint32_t *>(&hh);
+                    }
+                    *reinterpret_cast<uint4 *>(q_s + (c64 >> 3) * 8192 + row * 128 + (((c64 & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                }
+            }
+            if (bad) set_error(CSA2_DEVERR_Q_RANGE);
+            fence_proxy_async_smem();
+            named_bar_sync(3, kPxSoftWarps * 32);  // qrow_s may be written again
+            if (lane == 0) mbar_arrive_cluster(q_full_addr);
+        };
+        int32_t q_row, sees, next_q_row = -1, next_sees = 0;
+        load_q(w.t, q_row, sees);
+        float m_run = -INFINITY, l_run = 0.0f;
+        for (int i = 0; i < n && ok; ++i) {
+            const bool last = i == n - 1 || w.last();
+            PxWalk wn = w;
+            ok = mbar_wait_cluster(&s_full[i & 1], ((uint32_t)i >> 1) & 1u);
+            tc_fence_after();
+            if (i + 1 < n) {
+                wn.next(p);
+                // Q is free once S of the strip's last tile is done
+                if (last) load_q(wn.t, next_q_row, next_sees);
+            }
+            const uint32_t ts = lane_addr + kColS + 128 * (i & 1);
+            // scores of this thread that count: a bit each
+            uint32_t bits[4];
+            const int lim = min(max(sees - w.tile * kPxTile - 128 * half, 0), 128);
+            bool all = true;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int m = lim - 32 * k;
+                bits[k] = valid[(i & 3) * 8 + half * 4 + k] & (m >= 32 ? 0xFFFFFFFFu : m <= 0 ? 0u : (1u << m) - 1u);
+                all = all && bits[k] == 0xFFFFFFFFu;
+            }
+            all = __all_sync(0xFFFFFFFFu, all);
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v[32];
+                tmem_ld32(ts + 32 * k, v);
+                tmem_wait_ld();
+                if (all) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]) * p.scale_log2);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (bits[k] >> j & 1u) top = fmaxf(top, __uint_as_float(v[j]) * p.scale_log2);
+                }
+            }
+            // the row's other half
+            xch[(i & 1) * 128 + tid] = top;
+            named_bar_sync(pair_bar, 64);
+            top = fmaxf(top, xch[(i & 1) * 128 + (tid ^ 64)]);
+            float alpha = 1.0f;
+            const bool raise = top > m_run + kPxRescale || (m_run == -INFINITY && top > -INFINITY);
+            if (raise) {
+                if (m_run != -INFINITY) alpha = ex2(m_run - top);
+                m_run = top;
+                l_run *= alpha;
+            }
+            // P is free and O complete once the products of the tile before are done
+            if (i > 0 && ok) ok = mbar_wait_cluster(pv_done, (uint32_t)(i - 1) & 1u);
+            tc_fence_after();
+            if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+#pragma unroll 1
+                for (int k = 0; k < 256; k += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + k, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+                    tmem_st32(lane_addr + k, v);
+                }
+                tmem_wait_st();
+            }
+            const float at = m_run == -INFINITY ? 0.0f : m_run;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v[32];
+                tmem_ld32(ts + 32 * k, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q8 = 0; q8 < 4; ++q8) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int x = q8 * 8 + 2 * j;
+                        float a = ex2(fmaf(__uint_as_float(v[x]), p.scale_log2, -at));
+                        float b = ex2(fmaf(__uint_as_float(v[x + 1]), p.scale_log2, -at));
+                        if (!all) {
+                            a = bits[k] >> x & 1u ? a : 0.0f;
+                            b = bits[k] >> (x + 1) & 1u ? b : 0.0f;
+                        }
+                        sum[j] += a + b;
+                        // f16 probabilities: 2^-11 relative, what the products take
+                        const __half2 hh = __floats2half2_rn(a, b);
+                        pk[j] = *reinterpret_cast<const uint32_t *>(&hh);
+                    }
+                    const int piece = (k & 1) * 4 + q8;
+                    *reinterpret_cast<uint4 *>(p_s + (2 * half + (k >> 1)) * 8192 + r * 128 + ((piece ^ (r & 7)) << 4)) =
+                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(p_full_addr);
+            if (last) {
+                // the strip's partial of this run
+                xch[256 + tid] = l_run;
+                named_bar_sync(pair_bar, 64);
+                const float l = l_run + xch[256 + (tid ^ 64)];
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                if (ok) ok = mbar_wait_cluster(pv_done, (uint32_t)i & 1u);
+                tc_fence_after();
+                const int row = 64 * rank + r;
+                const bool pre = w.t.member0 >= 0;
+                const int64_t slot = pre ? ((int64_t)c + w.s) * kPxRows + row : ((int64_t)c + (w.s - w.n_pre)) * p.h + row;
+                float *dst = (pre ? p.pre_o : p.own_o) + slot * CSA2_D + 256 * half;
+                const bool mine = ok && q_row >= 0;
+#pragma unroll 1
+                for (int k = 0; k < 256; k += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + k, v);
+                    tmem_wait_ld();
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(dst + k + j) =
+                                make_float4(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv,
+                                            __uint_as_float(v[j + 2]) * inv, __uint_as_float(v[j + 3]) * inv);
+                    }
+                }
+                if (mine && half == 0)
+                    (pre ? p.pre_lse : p.own_lse)[slot] = l > 0.0f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                tc_fence_before();
+                m_run = -INFINITY;
+                l_run = 0.0f;
+                q_row = next_q_row;
+                sees = next_sees;
+            }
+            w = wn;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA of the pair leaves while the other's products or arrivals reach it
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// merge: one block per (member, query, head): o = sum_s w_s o_s / sum_s w_s,
+// w_s = exp(lse_s - max), over the partials of its prefix strip and its own.
+// ---------------------------------------------------------------------------
+constexpr int kPxMergeThreads = 128;
+constexpr int kPxMergeParts = 512;  // at most two strips over all pairs
+
+__global__ void __launch_bounds__(kPxMergeThreads) k_prefix_merge(PrefixParams p) {
+    __shared__ float wgt[kPxMergeParts];
+    __shared__ float red[2][4];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const int32_t i = blockIdx.x, head = blockIdx.y;
+    const int32_t j = i / p.q_per_seq, qi = i - j * p.q_per_seq;
+    const int32_t g = p.member_group[j];
+    if (g < 0) return;
+    const int64_t u = (int64_t)p.members[j] * p.q_per_seq + qi;
+    if (u >= p.nq) return;
+    const int64_t total = *p.total_tiles;
+    const int32_t pairs = px_pairs(p.pairs, total);
+    int32_t na = 0, nb = 0;
+    int64_t a0 = 0, b0 = 0;  // first rows of the partials
+    const int32_t s0 = p.group_strip[g];
+    if (s0 >= 0) {
+        const int32_t x = ((j - p.group_begin[g]) * p.q_per_seq + qi) * p.h + head;
+        const int32_t s = s0 + x / kPxRows;
+        const PrefixStrip t = p.strips[s];
+        const int32_t c = px_owner(total, pairs, t.tile0);
+        na = px_owner(total, pairs, t.tile0 + t.ntiles - 1) - c + 1;
+        a0 = ((int64_t)c + s) * kPxRows + x % kPxRows;
+    }
+    const PrefixStrip t = p.strips[p.max_pre + i];
+    if (t.ntiles > 0) {
+        const int32_t c = px_owner(total, pairs, t.tile0);
+        nb = px_owner(total, pairs, t.tile0 + t.ntiles - 1) - c + 1;
+        b0 = ((int64_t)c + i) * p.h + head;
+    }
+    const int32_t np = na + nb;
+    if (np > kPxMergeParts) {
+        if (tid == 0) set_error(CSA2_DEVERR_SELECT);
+        return;
+    }
+    float top = -INFINITY;
+    for (int s = tid; s < np; s += kPxMergeThreads) {
+        const float v = s < na ? p.pre_lse[a0 + (int64_t)s * kPxRows] : p.own_lse[b0 + (int64_t)(s - na) * p.h];
+        wgt[s] = v;
+        top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if ((tid & 31) == 0) red[0][tid >> 5] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    float sum = 0.0f;
+    for (int s = tid; s < np; s += kPxMergeThreads) {
+        const float v = top == -INFINITY ? 0.0f : expf(wgt[s] - top);
+        wgt[s] = v;
+        sum += v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 8;
+    for (int s1 = 0; s1 < np; s1 += kBatch) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+            const int x = s1 + s;
+            if (x < np)
+                v[s] = *(reinterpret_cast<const float4 *>(x < na ? p.pre_o + (a0 + (int64_t)x * kPxRows) * CSA2_D
+                                                                 : p.own_o + (b0 + (int64_t)(x - na) * p.h) * CSA2_D) + tid);
+        }
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s)
+            if (s1 + s < np) {
+                const float w = wgt[s1 + s];
+                acc.x = fmaf(w, v[s].x, acc.x);
+                acc.y = fmaf(w, v[s].y, acc.y);
+                acc.z = fmaf(w, v[s].z, acc.z);
+                acc.w = fmaf(w, v[s].w, acc.w);
+            }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int64_t row = u * p.h + head;
+    const uint32_t lo = (uint32_t)f32_to_bf16_bits(acc.x * inv) | ((uint32_t)f32_to_bf16_bits(acc.y * inv) << 16);
+    const uint32_t hi = (uint32_t)f32_to_bf16_bits(acc.z * inv) | ((uint32_t)f32_to_bf16_bits(acc.w * inv) << 16);
+    *(reinterpret_cast<uint2 *>(p.o + row * CSA2_D) + tid) = make_uint2(lo, hi);
+    if (tid == 0 && p.lse) p.lse[row] = sum > 0.0f ? top + logf(sum) : -INFINITY;
 }
 
 }  // namespace csa2
