@@ -1647,7 +1647,11 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     p.swa_end = has_swa ? swa_end : nullptr;
     p.o = static_cast<uint16_t *>(o_bf16);
     p.lse = lse;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    // the kernel takes maxima of unscaled scores and -inf for masked ones, so
+    // the sign goes into q, and a scale of 0 (all probabilities equal) becomes
+    // one that scales every finite score to where exp2 is 1
+    p.scale_log2 = std::max(std::fabs(softmax_scale) * 1.4426950408889634f, 1e-30f);
+    p.q_flip = softmax_scale < 0.0f ? 0x80008000u : 0u;
     p.nq = nq;
     p.q_per_seq = q_per_seq;
     p.h = h;

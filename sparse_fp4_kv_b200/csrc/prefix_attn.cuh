@@ -65,7 +65,8 @@ struct PrefixParams {
     const int32_t *swa_begin, *swa_end;
     uint16_t *o;
     float *lse;        // nullable
-    float scale_log2;  // softmax scale * log2(e)
+    float scale_log2;  // |softmax scale| * log2(e), above 0
+    uint32_t q_flip;   // sign bits of two f16 values when the softmax scale is negative
     int32_t nq, q_per_seq, h, w_max, n_members, n_groups, pairs;
     // workspace
     int64_t *total_tiles;   // [1]
@@ -85,7 +86,7 @@ constexpr int kPxRows = 128;  // query rows of a strip
 constexpr int kPxSoftWarps = 4;
 constexpr int kPxLoadWarps = 8;
 constexpr int kPxMmaWarp = kPxSoftWarps + kPxLoadWarps;
-constexpr int kPxThreads = (kPxMmaWarp + 1) * 32;
+constexpr int kPxThreads = 16 * 32;  // three idle warps fill the last group of four
 constexpr int kPxSlots = 4;
 constexpr int kPxSlotBytes = 32768;
 constexpr int kPxQBytes = 64 * CSA2_D * 2;
@@ -150,6 +151,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
     set_error(CSA2_DEVERR_WAIT_TIMEOUT);
     return false;
+}
+// Registers of the calling group of four warps. The four groups' shares sum up
+// to what the block is launched with (4 x 128): softmax 208, rows 120 each,
+// products 64 (with fewer some spill, and a spill is a trip to L2: the carve-out
+// for shared memory leaves little L1).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -363,68 +376,105 @@ struct PxWalk {
     __device__ __forceinline__ int value_chunks() const { return (min(kPxTile, t.rows - tile * kPxTile) + 63) >> 6; }
 };
 
-// Where row r of the walk's tile lies: >= 0 a physical cache row, kPxNone no
-// row, else -2 - slot of the window ring.
+// Where a row of a tile lies: >= 0 a physical cache row, kPxNone no row, else
+// -2 - slot of the window ring. Resolved in two steps, so that the page-table
+// load is in flight while a group of chunks is handled: px_look gives, for an
+// entry, the row within its page and starts the load of the page number.
 constexpr int32_t kPxNone = -1;
-__device__ __forceinline__ int32_t px_resolve(const PrefixParams &p, const PxWalk &w, int r) {
+struct PxLook {
+    int32_t code, page;
+};
+__device__ __forceinline__ void px_look(const PrefixParams &p, const PxWalk &w, int r, PxLook &x) {
     const int32_t j = w.tile * kPxTile + r;
-    if (j >= w.t.rows) return kPxNone;
+    x.code = kPxNone;
+    x.page = -1;
     if (j < w.t.entries) {
-        const int64_t row = physical_row(p.kv, w.t.seq, (int64_t)w.t.t_base + j);
-        if (row < 0) {
-            set_error(CSA2_DEVERR_BAD_ROW);
-            return kPxNone;
-        }
-        return (int32_t)row;
+        const uint32_t t = (uint32_t)w.t.t_base + (uint32_t)j;  // below max_pages * page_size (px_limit)
+        const uint32_t page = t / (uint32_t)p.kv.page_size;
+        x.code = (int32_t)(t - page * (uint32_t)p.kv.page_size);
+        x.page = p.kv.page_table[(int64_t)w.t.seq * p.kv.max_pages + page];
+    } else if (j < w.t.rows) {
+        int64_t sl = (int64_t)w.t.w_begin + (j - w.t.entries);  // below twice the stride
+        if (sl >= p.swa_seq_stride) sl -= p.swa_seq_stride;
+        x.code = -2 - (int32_t)sl;
     }
-    int64_t sl = (int64_t)w.t.w_begin + (j - w.t.entries);  // below twice the stride
-    if (sl >= p.swa_seq_stride) sl -= p.swa_seq_stride;
-    return -2 - (int32_t)sl;
+}
+__device__ __forceinline__ int32_t px_row(const PrefixParams &p, const PxLook &x) {
+    if (x.code < 0) return x.code;
+    const int64_t row = (int64_t)x.page * p.kv.page_size + x.code;
+    if (x.page >= 0 && row < p.kv.rows_cap) return (int32_t)row;
+    set_error(CSA2_DEVERR_BAD_ROW);
+    return kPxNone;
 }
 
-// 64 values of a row: raw bytes as loaded.
+// A lane's share of a chunk: four units of 32 values (16 bytes of codes and 2
+// of scales, or 32 bytes of a window row), of rows that are 8 (keys) or 4
+// (values) apart. The lanes of a warp cover whole 64- or 128-byte runs of rows
+// (a lane with a row of its own would touch 32 lines per load: measured, that
+// made the loads the bound), and a quarter warp four rows of one block, so that
+// its 16-byte stores meet the eight bank groups of the swizzle. The loads are
+// predicated instructions on registers that nothing else merges into, so none
+// waits for another.
 struct PxRaw {
-    uint4 v[4];
-    uint32_t sc;
-    int32_t src;
+    uint32_t v[4][4], sc[4];
 };
-__device__ __forceinline__ void px_fetch(const PrefixParams &p, const uint8_t *swa_seq, int32_t src, int blk, PxRaw &raw) {
-    raw.src = src;
-    if (src >= 0) {
-        const uint4 *c = reinterpret_cast<const uint4 *>(p.kv.codes + (int64_t)src * (CSA2_D / 2) + blk * 32);
-        raw.v[0] = __ldg(c);
-        raw.v[1] = __ldg(c + 1);
-        raw.sc = __ldg(reinterpret_cast<const uint32_t *>(p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + blk * 4));
-    } else if (src != kPxNone) {
-        const uint4 *w = reinterpret_cast<const uint4 *>(swa_seq + (int64_t)(-2 - src) * CSA2_D + blk * 64);
+__device__ __forceinline__ void px_ld16(uint32_t *v, const void *at, bool take) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
+        : "l"(at), "r"((int)take));
+}
+__device__ __forceinline__ void px_ld4(uint32_t &v, const void *at, bool take) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)take));
+}
+// All four units when their rows lie STEP apart in the cache: at, sc are the
+// first unit's codes and the word that holds its scales.
+template <int STEP>
+__device__ __forceinline__ void px_fetch_run(const uint8_t *at, const uint8_t *sc, PxRaw &raw, bool take) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) raw.v[j] = __ldg(w + j);
+    for (int u = 0; u < 4; ++u) {
+        px_ld16(raw.v[u], at + u * STEP * (CSA2_D / 2), take);
+        px_ld4(raw.sc[u], sc + u * STEP * (CSA2_D / CSA2_BLOCK), take);
     }
 }
-// Dequantised into a 128-byte row of a swizzled block (dst: the row, r8: row & 7).
-__device__ __forceinline__ void px_store(const PxRaw &raw, uint8_t *dst, int r8) {
-    if (raw.src >= 0) {
-        const uint32_t w[8] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w, raw.v[1].x, raw.v[1].y, raw.v[1].z, raw.v[1].w};
+// Unit u alone: values d0 .. d0 + 31 of row src. Of a window row's 32 bytes the
+// first 16 are fetched; the rest, of the same sector, when the unit is stored
+// (window rows are few, and registers limit the fetching warps).
+__device__ __forceinline__ void px_fetch(const PrefixParams &p, const uint8_t *swa_seq, int32_t src, int d0, PxRaw &raw, int u) {
+    const bool fp4 = src >= 0;
+    const uint8_t *at = fp4 ? p.kv.codes + (int64_t)src * (CSA2_D / 2) + d0 / 2 : swa_seq + (int64_t)(-2 - src) * CSA2_D + d0;
+    px_ld16(raw.v[u], at, src != kPxNone);
+    px_ld4(raw.sc[u], p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3), fp4);
+}
+// A unit of FP4 values dequantised into four 16-byte pieces at dst + off[j].
+// sc: its two scales.
+__device__ __forceinline__ void px_store_fp4(const uint32_t (&raw)[4], uint32_t sc, uint8_t *dst, const uint32_t (&off)[4]) {
+    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)sc);
+    const uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t sb = (raw.sc >> (8 * (j >> 1))) & 0xFFu;
-            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(sb | (sb << 8)));
-            uint32_t h[4];
-            e2m1x8_to_f16x8(w[j], h);
-            *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) =
-                make_uint4(hmul2_u32(h[0], s2), hmul2_u32(h[1], s2), hmul2_u32(h[2], s2), hmul2_u32(h[3], s2));
-        }
-    } else if (raw.src != kPxNone) {
-        const uint32_t w[16] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w, raw.v[1].x, raw.v[1].y, raw.v[1].z, raw.v[1].w,
-                                raw.v[2].x, raw.v[2].y, raw.v[2].z, raw.v[2].w, raw.v[3].x, raw.v[3].y, raw.v[3].z, raw.v[3].w};
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h[4];
+        e2m1x8_to_f16x8(raw[j], h);
+        *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(hmul2_u32(h[0], f[j >> 1]), hmul2_u32(h[1], f[j >> 1]),
+                                                             hmul2_u32(h[2], f[j >> 1]), hmul2_u32(h[3], f[j >> 1]));
+    }
+}
+// A unit of any row.
+__device__ __forceinline__ void px_store(const uint32_t (&raw)[4], uint32_t sc, int32_t src, const uint8_t *swa_at, uint8_t *dst,
+                                         const uint32_t (&off)[4]) {
+    if (src >= 0) {
+        px_store_fp4(raw, sc, dst, off);
+    } else if (src != kPxNone) {
+        const uint4 m = __ldg(reinterpret_cast<const uint4 *>(swa_at + (int64_t)(-2 - src) * CSA2_D + 16));
+        const uint32_t w[8] = {raw[0], raw[1], raw[2], raw[3], m.x, m.y, m.z, m.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) =
-                make_uint4(e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
-                           e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(
+                e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
+                e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(dst + ((j ^ r8) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -454,17 +504,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     uint8_t *p_s = q_s + kPxQBytes;              // [4 blocks of 64 cache rows][64 rows][128 B]
     uint8_t *ring = p_s + kPxPBytes;             // [kPxSlots][32 KiB]
     uint8_t *misc = ring + kPxSlots * kPxSlotBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots] (first CTA's: both CTAs' loaders arrive)
-    uint64_t *empty = full + kPxSlots;                    // [kPxSlots]
-    uint64_t *s_full = empty + kPxSlots;                  // [2]
+    // what a CTA's own warps arrive at, and in the first CTA the same of the
+    // second, forwarded by its last warp (an arrival at another CTA's barrier
+    // waits for all loads in flight of its warp: 930 cycles for a warp that
+    // fetches rows, measured)
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots]
+    uint64_t *p_full = full + kPxSlots;
+    uint64_t *q_full = p_full + 1;
+    uint64_t *peer_full = q_full + 1;  // [kPxSlots]
+    uint64_t *peer_p = peer_full + kPxSlots;
+    uint64_t *peer_q = peer_p + 1;
+    uint64_t *empty = peer_q + 1;  // [kPxSlots]
+    uint64_t *s_full = empty + kPxSlots;  // [2]
     uint64_t *pv_done = s_full + 2;
-    uint64_t *p_full = pv_done + 1;  // (first CTA's)
-    uint64_t *q_full = p_full + 1;   // (first CTA's)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 1);
-    uint32_t *valid = tmem_slot + 2;                            // [4 tiles][8 words] resolved rows
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 1);
+    uint32_t *valid = tmem_slot + 2;  // 16-byte aligned:                          // [4 tiles][8 words] resolved rows
     float *xch = reinterpret_cast<float *>(valid + 32);         // [3][128] maxima of even and odd tiles, sums
-    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 384);   // [64]
-    static_assert(8 * (2 * kPxSlots + 5) + 8 + 128 + 1536 + 256 <= kPxMisc, "misc");
+    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 256);   // [64], between the exchanges of sums
+    static_assert(8 * (3 * kPxSlots + 7) + 8 + 128 + 1536 <= kPxMisc && (8 * (3 * kPxSlots + 7) + 8) % 16 == 0, "misc");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
@@ -475,14 +532,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     }
     if (tid == 0) {
         for (int i = 0; i < kPxSlots; ++i) {
-            mbar_init(&full[i], 2 * kPxLoadWarps);
+            mbar_init(&full[i], kPxLoadWarps / 2);  // one set
+            mbar_init(&peer_full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(pv_done, 1);
-        mbar_init(p_full, 2 * kPxSoftWarps);
-        mbar_init(q_full, 2 * kPxSoftWarps);
+        mbar_init(p_full, kPxSoftWarps);
+        mbar_init(q_full, kPxSoftWarps);
+        mbar_init(peer_p, 1);
+        mbar_init(peer_q, 1);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -499,8 +559,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     const int n = c < pairs ? (int)(px_lo(total, pairs, c + 1) - x0) : 0;
     constexpr uint32_t kColS = 256;
 
-    if (n > 0 && warp == kPxMmaWarp) {
-        if (rank == 0 && lane == 0) {
+    if (warp >= kPxMmaWarp) {
+        regs_dec<64>();
+        if (n > 0 && warp == kPxMmaWarp && rank == 0 && lane == 0) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, 256, 0, 0), idesc_o = idesc_f16_f32(128, 256, 0, 1);
             const uint64_t a_q = make_sdesc(smem_u32(q_s), 16, 1024, kSw128);
             const uint64_t a_p = make_sdesc(smem_u32(p_s), 16, 1024, kSw128);
@@ -512,10 +573,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             uint32_t chunk = 0, strips = 0;
             bool ok = true;
             auto scores = [&](int i) {
-                if (i == 0 || wk.tile == 0) ok = ok && mbar_wait_cluster(q_full, strips++ & 1u);
+                if (i == 0 || wk.tile == 0) {
+                    ok = ok && mbar_wait(q_full, strips & 1u) && mbar_wait_cluster(peer_q, strips & 1u);
+                    ++strips;
+                }
                 for (int d = 0; d < 4 && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait_cluster(&full[slot], (chunk / kPxSlots) & 1u);
+                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u) && mbar_wait_cluster(&peer_full[slot], (chunk / kPxSlots) & 1u);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -533,12 +597,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     wk.next(p);
                     scores(i + 1);
                 }
-                ok = ok && mbar_wait_cluster(p_full, (uint32_t)i & 1u);
+                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u) && mbar_wait_cluster(peer_p, (uint32_t)i & 1u);
                 const bool fresh = i == 0 || wv.tile == 0;
                 const int nv = wv.value_chunks();
                 for (int d = 0; d < nv && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait_cluster(&full[slot], (chunk / kPxSlots) & 1u);
+                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u) && mbar_wait_cluster(&peer_full[slot], (chunk / kPxSlots) & 1u);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -553,97 +617,202 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 if (ok) tc_commit_pair(pv_done);
                 if (i + 1 < n) wv.next(p);
             }
+        } else if (n > 0 && warp == kPxMmaWarp && rank == 1 && lane == 0) {
+            // the same waits, in the same order, passed on
+            PxWalk wk, wv;
+            wk.begin(p, c, x0);
+            wv = wk;
+            uint32_t chunk = 0, strips = 0;
+            bool ok = true;
+            const uint32_t to_full = cluster_smem_addr(peer_full, 0), to_p = cluster_smem_addr(peer_p, 0), to_q = cluster_smem_addr(peer_q, 0);
+            auto chunks = [&](int m) {
+                for (int d = 0; d < m && ok; ++d, ++chunk) {
+                    const uint32_t slot = chunk % kPxSlots;
+                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
+                    if (ok) mbar_arrive_cluster(to_full + 8 * slot);
+                }
+            };
+            auto keys = [&](int i) {
+                if (i == 0 || wk.tile == 0) {
+                    ok = ok && mbar_wait(q_full, strips++ & 1u);
+                    if (ok) mbar_arrive_cluster(to_q);
+                }
+                chunks(4);
+            };
+            keys(0);
+            for (int i = 0; i < n && ok; ++i) {
+                if (i + 1 < n) {
+                    wk.next(p);
+                    keys(i + 1);
+                }
+                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u);
+                if (ok) mbar_arrive_cluster(to_p);
+                chunks(wv.value_chunks());
+                if (i + 1 < n) wv.next(p);
+            }
         }
         __syncwarp();
-    } else if (n > 0 && warp >= kPxSoftWarps) {
-        // ---- rows of the cache into the ring ----
-        const int lw = warp - kPxSoftWarps;
-        const int k_row = 16 * lw + (lane & 15), k_blk = lane >> 4;         // keys: 16 rows x 2 blocks a warp
-        const int v_row = 8 * lw + (lane & 7), v_blk = 4 * rank + (lane >> 3);  // values: 8 rows x 4 blocks
-        uint32_t full_addr[kPxSlots];
-#pragma unroll
-        for (int i = 0; i < kPxSlots; ++i) full_addr[i] = cluster_smem_addr(&full[i], 0);
+    } else if (warp >= kPxSoftWarps) {
+        regs_dec<120>();
+        if (n > 0) {
+        // ---- rows of the cache into the ring: two sets of four warps, the first
+        // with chunks 0 and 2 of a group of four, the second with 1 and 3 ----
+        const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
         PxWalk w;
         w.begin(p, c, x0);
-        // rows of a tile, resolved when its keys come up: the keys' one, the values' four
+        // the rows of a tile that this lane resolves: one of its keys (row 32 lw +
+        // lane of the CTA's half) and one of its values (row 64 d + 16 lw +
+        // (lane & 15), d = set for the lower lanes, set + 2 for the upper)
+        struct Look {
+            PxLook k, v;
+            int nv;
+            int32_t w_seq;
+        };
         struct Rows {
-            int32_t k, v[4];
+            int32_t k, v;
+            int nv;
+            bool k_run, v_run;  // the warp's 32 keys, its two runs of 16 values lie in a row in the cache
+            const uint8_t *swa;
+        };
+        auto look = [&]() {
+            Look x;
+            px_look(p, w, 128 * rank + 32 * lw + lane, x.k);
+            px_look(p, w, 64 * (2 * (lane >> 4) + set) + 16 * lw + (lane & 15), x.v);
+            x.nv = w.value_chunks();
+            x.w_seq = w.t.w_seq;
+            return x;
+        };
+        auto resolve = [&](int i, const Look &x) {
+            Rows r;
+            r.k = px_row(p, x.k);
+            r.v = px_row(p, x.v);
+            r.nv = x.nv;
+            r.swa = p.swa + (int64_t)x.w_seq * p.swa_seq_stride * CSA2_D;
+            const int32_t k0 = __shfl_sync(0xFFFFFFFFu, r.k, 0), v0 = __shfl_sync(0xFFFFFFFFu, r.v, lane & 16);
+            r.k_run = __all_sync(0xFFFFFFFFu, (int)(r.k >= 0) & (int)(r.k == k0 + lane));
+            r.v_run = __all_sync(0xFFFFFFFFu, (int)(r.v >= 0) & (int)(r.v == v0 + (lane & 15)));
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, r.v != kPxNone);
+            if (lane < 2) reinterpret_cast<uint16_t *>(valid + (i & 3) * 8)[4 * (2 * lane + set) + lw] = (uint16_t)(m >> (16 * lane));
+            return r;
+        };
+        PxRaw raw[2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                raw[d].sc[u] = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) raw[d].v[u][j] = 0u;
+            }
+        // A group of chunks in hand. One body for both kinds: the loop has to stay
+        // within the instruction cache. Lane l of a warp has
+        //   keys: rows 8 u + 4 (l / 8 % 2) + l / 2 % 4 of the warp's 32, units l / 16
+        //     (block) and l % 2 of the chunk's 128 values;
+        //   values: rows 4 u + l / 2 % 4 of its 16, units l / 8 and l % 2 of 256.
+        struct Group {
+            int32_t rows;  // this lane's resolved row
+            bool keys, run;
             int nv;
             const uint8_t *swa;
         };
-        auto resolve = [&](int i) {
-            Rows r;
-            r.k = px_resolve(p, w, 128 * rank + k_row);
-            r.nv = w.value_chunks();
-            r.swa = p.swa ? p.swa + (int64_t)w.t.w_seq * p.swa_seq_stride * CSA2_D : nullptr;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                r.v[d] = px_resolve(p, w, 64 * d + v_row);
-                const uint32_t m = __ballot_sync(0xFFFFFFFFu, r.v[d] != kPxNone) & 0xFFu;
-                // rows 64 d + 8 lw .. + 7: a byte of word 2 d + lw / 4
-                if (lane == 0) reinterpret_cast<uint8_t *>(valid + (i & 3) * 8)[8 * d + lw] = (uint8_t)m;
-            }
-            return r;
+        const int k_sub = 4 * ((lane >> 3) & 1) + ((lane >> 1) & 3), v_sub = (lane >> 1) & 3;
+        auto source = [&](const Group &g, int d, int u) {
+            return __shfl_sync(0xFFFFFFFFu, g.rows, g.keys ? 8 * u + k_sub : 16 * d + 4 * u + v_sub);
         };
-        uint32_t chunk = 0;
-        bool ok = true;
-        PxRaw raw[2];
-        auto fetch = [&](const Rows &r, bool keys, int d, PxRaw &x) {
-            if (keys) px_fetch(p, r.swa, r.k, 2 * d + k_blk, x);
-            else if (d < r.nv) px_fetch(p, r.swa, r.v[d], v_blk, x);
+        auto value0 = [&](const Group &g, int d) {  // the first value of the lane's units
+            return (g.keys ? 128 * (2 * d + set) + 64 * (lane >> 4) : 256 * (int)rank + 64 * (lane >> 3)) + 32 * (lane & 1);
         };
-        auto put = [&](const Rows &r, bool keys, int d, const PxRaw &x) {
-            if (!keys && d >= r.nv) return;
-            const uint32_t slot = chunk % kPxSlots, round = chunk / kPxSlots;
-            if (round > 0 && ok && !mbar_wait_cluster(&empty[slot], (round - 1) & 1u)) ok = false;
-            uint8_t *s = ring + slot * kPxSlotBytes;
-            if (ok) {
-                if (keys) px_store(x, s + k_blk * 16384 + k_row * 128, k_row & 7);
-                else px_store(x, s + (lane >> 3) * 8192 + v_row * 128, v_row & 7);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(slot == 0 ? full_addr[0] : slot == 1 ? full_addr[1] : slot == 2 ? full_addr[2] : full_addr[3]);
-            ++chunk;
-        };
-        // groups of four chunks: K(0), K(1), V(0), K(2), V(1), ...; the first two
-        // chunks of a group are fetched under the last two of the group before
-        auto group = [&](const Rows &r, bool keys, const Rows &rn, bool next_keys, bool has_next) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                put(r, keys, d, raw[d & 1]);
-                if (d < 2) fetch(r, keys, d + 2, raw[d & 1]);
-                else if (has_next) fetch(rn, next_keys, d - 2, raw[d & 1]);
-            }
-        };
-        Rows cur = resolve(0), nxt = cur;
-        fetch(cur, true, 0, raw[0]);
-        fetch(cur, true, 1, raw[1]);
-        if (n > 1) {
-            w.next(p);
-            nxt = resolve(1);
-        }
-        group(cur, true, n > 1 ? nxt : cur, n > 1, true);
-        if (n > 1) group(nxt, true, cur, false, true);
-        for (int i = 0; i < n && ok; ++i) {
-            // V(i), then K(i + 2)
-            Rows after = nxt;
-            if (i + 2 < n) {
-                w.next(p);
-                after = resolve(i + 2);
-                group(cur, false, after, true, true);
-                group(after, true, nxt, false, true);
+        auto fetch = [&](const Group &g, int d, PxRaw &x) {
+            const int d0 = value0(g, d);
+            if (g.run) {
+                const int64_t row = (int64_t)__shfl_sync(0xFFFFFFFFu, g.rows, g.keys ? 0 : 16 * d) + (g.keys ? k_sub : v_sub);
+                const uint8_t *at = p.kv.codes + row * (CSA2_D / 2) + d0 / 2;
+                const uint8_t *sc = p.kv.scales + row * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3);
+                const bool take = row >= 0 && row + (g.keys ? 24 : 12) < p.kv.rows_cap;
+                if (g.keys) px_fetch_run<8>(at, sc, x, take);
+                else px_fetch_run<4>(at, sc, x, take);
+                if (!take) set_error(CSA2_DEVERR_SELECT);
             } else {
-                group(cur, false, nxt, false, i + 1 < n);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) px_fetch(p, g.swa, source(g, d, u), d0, x, u);
             }
+        };
+        // Groups in the order of the products: K(0), K(1), V(0), K(2), V(1), ...,
+        // K(n - 1), V(n - 2), V(n - 1). The rows of a tile are resolved with its
+        // keys; those of the values wait in (q0, q1) for their turn.
+        Rows q0 = resolve(0, look()), q1 = q0;
+        int queued = 1, resolved = 1;
+        Look ahead;
+        auto look_ahead = [&]() {
+            if (resolved < n) {
+                w.next(p);
+                ahead = look();
+            }
+        };
+        look_ahead();
+        Group cur{q0.k, true, q0.k_run, q0.nv, q0.swa};
+        fetch(cur, 0, raw[0]);
+        fetch(cur, 1, raw[1]);
+        uint32_t chunk = 0;  // first of the group
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < 2 * n && ok; ++j) {
+            const bool more = j + 1 < 2 * n;
+            Group nxt = cur;
+            if ((j & 1) == 0 && j + 2 < 2 * n) {  // K
+                const Rows r = resolve(resolved, ahead);
+                ++resolved;
+                look_ahead();
+                nxt = Group{r.k, true, r.k_run, r.nv, r.swa};
+                if (queued == 0) q0 = r;
+                else q1 = r;
+                ++queued;
+            } else if (more) {  // V
+                nxt = Group{q0.v, false, q0.v_run, q0.nv, q0.swa};
+                q0 = q1;
+                --queued;
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                if (cur.keys || 2 * d + set < cur.nv) {
+                    const uint32_t at = chunk + 2 * d + set, slot = at % kPxSlots, round = at / kPxSlots;
+                    if (round > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], (round - 1) & 1u));
+                    uint8_t *s = ring + slot * kPxSlotBytes;
+                    if (ok) {
+                        // blocks of 64 values: keys [128 rows][128 B], values [64 rows][128 B]
+                        s += cur.keys ? (lane >> 4) * 16384 + (32 * lw + k_sub) * 128 : (lane >> 3) * 8192 + (16 * lw + v_sub) * 128;
+                        const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (cur.keys ? k_sub : v_sub)) << 4;
+                        const uint32_t even[4] = {o0, o0 ^ 16u, o0 ^ 32u, o0 ^ 48u};
+                        const uint32_t flip = cur.keys ? 0u : 64u;  // rows 4 further on swap the halves of the swizzle
+                        const uint32_t odd[4] = {even[0] ^ flip, even[1] ^ flip, even[2] ^ flip, even[3] ^ flip};
+                        const int step = cur.keys ? 8 * 128 : 4 * 128;
+                        if (cur.run) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                px_store_fp4(raw[d].v[u], raw[d].sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? odd : even);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                px_store(raw[d].v[u], raw[d].sc[u] >> (16 * (lane & 1)), source(cur, d, u), cur.swa + value0(cur, d), s + u * step,
+                                         u & 1 ? odd : even);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[slot]);
+                }
+                if (more) fetch(nxt, d, raw[d]);
+            }
+            chunk += cur.keys ? 4 : cur.nv;
             cur = nxt;
-            nxt = after;
         }
-    } else if (n > 0) {
+        }
+    } else {
+        regs_inc<208>();
+        if (n > 0) {
         // ---- softmax: this thread has row 64 * rank + (tid & 63) of a strip and half of its scores ----
         const int r = tid & 63, half = tid >> 6;
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t p_full_addr = cluster_smem_addr(p_full, 0), q_full_addr = cluster_smem_addr(q_full, 0);
         const int pair_bar = 1 + (warp & 1);  // warps w and w + 2 have the same rows
         PxWalk w;
         w.begin(p, c, x0);
@@ -673,7 +842,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                         // 65536 and more (0x4780 and up, infinities and NaN too) have no finite f16 value
                         bad |= (w4[j] & 0x7FFFu) >= 0x4780u || ((w4[j] >> 16) & 0x7FFFu) >= 0x4780u;
                         const __half2 hh = __floats2half2_rn(__uint_as_float(w4[j] << 16), __uint_as_float(w4[j] & 0xFFFF0000u));
-                        o4[j] = *reinterpret_cast<const uint32_t *>(&hh);
+                        o4[j] = *reinterpret_cast<const uint32_t *>(&hh) ^ p.q_flip;
                     }
                     *reinterpret_cast<uint4 *>(q_s + (c64 >> 3) * 8192 + row * 128 + (((c64 & 7) ^ (row & 7)) << 4)) =
                         make_uint4(o4[0], o4[1], o4[2], o4[3]);
@@ -682,15 +851,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             if (bad) set_error(CSA2_DEVERR_Q_RANGE);
             fence_proxy_async_smem();
             named_bar_sync(3, kPxSoftWarps * 32);  // qrow_s may be written again
-            if (lane == 0) mbar_arrive_cluster(q_full_addr);
+            if (lane == 0) mbar_arrive(q_full);
         };
         int32_t q_row, sees, next_q_row = -1, next_sees = 0;
         load_q(w.t, q_row, sees);
         float m_run = -INFINITY, l_run = 0.0f;
-        for (int i = 0; i < n && ok; ++i) {
+        // after a wait that gave up the loop goes on without waiting: the other
+        // warps count on this one at their barriers
+        for (int i = 0; i < n; ++i) {
             const bool last = i == n - 1 || w.last();
             PxWalk wn = w;
-            ok = mbar_wait_cluster(&s_full[i & 1], ((uint32_t)i >> 1) & 1u);
+            if (ok) ok = mbar_wait(&s_full[i & 1], ((uint32_t)i >> 1) & 1u);
             tc_fence_after();
             if (i + 1 < n) {
                 wn.next(p);
@@ -698,32 +869,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 if (last) load_q(wn.t, next_q_row, next_sees);
             }
             const uint32_t ts = lane_addr + kColS + 128 * (i & 1);
-            // scores of this thread that count: a bit each
-            uint32_t bits[4];
+            // scores of this thread that do not count become -inf, in TMEM and by a
+            // loop of its own, so that the common path has no masks
             const int lim = min(max(sees - w.tile * kPxTile - 128 * half, 0), 128);
-            bool all = true;
+            const uint4 vw = *reinterpret_cast<const uint4 *>(valid + (i & 3) * 8 + half * 4);
+            if (__any_sync(0xFFFFFFFFu, lim < 128 || (vw.x & vw.y & vw.z & vw.w) != 0xFFFFFFFFu)) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const int m = lim - 32 * k;
+                    const uint32_t word = k == 0 ? vw.x : k == 1 ? vw.y : k == 2 ? vw.z : vw.w;
+                    const uint32_t bits = word & (m >= 32 ? 0xFFFFFFFFu : m <= 0 ? 0u : (1u << m) - 1u);
+                    uint32_t v[32];
+                    tmem_ld32(ts + 32 * k, v);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int m = lim - 32 * k;
-                bits[k] = valid[(i & 3) * 8 + half * 4 + k] & (m >= 32 ? 0xFFFFFFFFu : m <= 0 ? 0u : (1u << m) - 1u);
-                all = all && bits[k] == 0xFFFFFFFFu;
-            }
-            all = __all_sync(0xFFFFFFFFu, all);
-            float top = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[32];
-                tmem_ld32(ts + 32 * k, v);
-                tmem_wait_ld();
-                if (all) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]) * p.scale_log2);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (bits[k] >> j & 1u) top = fmaxf(top, __uint_as_float(v[j]) * p.scale_log2);
+                    for (int j = 0; j < 32; ++j) v[j] = bits >> j & 1u ? v[j] : 0xFF800000u;
+                    tmem_st32(ts + 32 * k, v);
                 }
+                tmem_wait_st();
             }
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                uint32_t v[32], y[32];
+                tmem_ld32(ts + 32 * k, v);
+                tmem_ld32(ts + 32 * k + 32, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) t4[j & 3] = fmaxf(t4[j & 3], fmaxf(__uint_as_float(v[j]), __uint_as_float(y[j])));
+            }
+            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
             // the row's other half
             xch[(i & 1) * 128 + tid] = top;
             named_bar_sync(pair_bar, 64);
@@ -735,9 +910,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 m_run = top;
                 l_run *= alpha;
             }
-            // P is free and O complete once the products of the tile before are done
-            if (i > 0 && ok) ok = mbar_wait_cluster(pv_done, (uint32_t)(i - 1) & 1u);
+            // P in registers while the products of the tile before still read the last one
+            const float at = m_run == -INFINITY ? 0.0f : m_run;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t pk[64];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v[32];
+                tmem_ld32(ts + 32 * k, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float a = ex2(fmaf(__uint_as_float(v[2 * j]), p.scale_log2, -at));
+                    const float b = ex2(fmaf(__uint_as_float(v[2 * j + 1]), p.scale_log2, -at));
+                    sum[j & 3] += a + b;
+                    // f16 probabilities: 2^-11 relative, what the products take
+                    const __half2 hh = __floats2half2_rn(a, b);
+                    pk[16 * k + j] = *reinterpret_cast<const uint32_t *>(&hh);
+                }
+            }
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (i > 0 && ok) ok = mbar_wait(pv_done, (uint32_t)(i - 1) & 1u);
             tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+                *reinterpret_cast<uint4 *>(p_s + (2 * half + (x >> 3)) * 8192 + r * 128 + (((x & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
             if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
 #pragma unroll 1
                 for (int k = 0; k < 256; k += 32) {
@@ -750,47 +948,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 }
                 tmem_wait_st();
             }
-            const float at = m_run == -INFINITY ? 0.0f : m_run;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[32];
-                tmem_ld32(ts + 32 * k, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q8 = 0; q8 < 4; ++q8) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int x = q8 * 8 + 2 * j;
-                        float a = ex2(fmaf(__uint_as_float(v[x]), p.scale_log2, -at));
-                        float b = ex2(fmaf(__uint_as_float(v[x + 1]), p.scale_log2, -at));
-                        if (!all) {
-                            a = bits[k] >> x & 1u ? a : 0.0f;
-                            b = bits[k] >> (x + 1) & 1u ? b : 0.0f;
-                        }
-                        sum[j] += a + b;
-                        // f16 probabilities: 2^-11 relative, what the products take
-                        const __half2 hh = __floats2half2_rn(a, b);
-                        pk[j] = *reinterpret_cast<const uint32_t *>(&hh);
-                    }
-                    const int piece = (k & 1) * 4 + q8;
-                    *reinterpret_cast<uint4 *>(p_s + (2 * half + (k >> 1)) * 8192 + r * 128 + ((piece ^ (r & 7)) << 4)) =
-                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-            }
-            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(p_full_addr);
+            if (lane == 0) mbar_arrive(p_full);
             if (last) {
                 // the strip's partial of this run
                 xch[256 + tid] = l_run;
                 named_bar_sync(pair_bar, 64);
                 const float l = l_run + xch[256 + (tid ^ 64)];
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                if (ok) ok = mbar_wait_cluster(pv_done, (uint32_t)i & 1u);
+                if (ok) ok = mbar_wait(pv_done, (uint32_t)i & 1u);
                 tc_fence_after();
                 const int row = 64 * rank + r;
                 const bool pre = w.t.member0 >= 0;
@@ -819,6 +987,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 sees = next_sees;
             }
             w = wn;
+        }
         }
     }
     tc_fence_before();
