@@ -128,30 +128,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, "
-        "0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// mbar_wait with cluster scope (same limit and error).
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-#pragma unroll 1
-    for (uint32_t n = 0; n < kWaitMaxPolls && global_ns() - t0 < kWaitNs; ++n) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        __nanosleep(64);
-    }
-    set_error(CSA2_DEVERR_WAIT_TIMEOUT);
-    return false;
-}
 // Registers of the calling group of four warps. The four groups' shares sum up
 // to what the block is launched with (4 x 128): softmax 208, rows 120 each,
 // products 64 (with fewer some spill, and a spill is a trip to L2: the carve-out
@@ -504,24 +480,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     uint8_t *p_s = q_s + kPxQBytes;              // [4 blocks of 64 cache rows][64 rows][128 B]
     uint8_t *ring = p_s + kPxPBytes;             // [kPxSlots][32 KiB]
     uint8_t *misc = ring + kPxSlots * kPxSlotBytes;
-    // what a CTA's own warps arrive at, and in the first CTA the same of the
-    // second, forwarded by its last warp (an arrival at another CTA's barrier
-    // waits for all loads in flight of its warp: 930 cycles for a warp that
-    // fetches rows, measured)
+    // Barriers at which a CTA's own warps arrive; the last warp of the second CTA
+    // passes its CTA's arrivals on to the first CTA's (an arrival at another
+    // CTA's barrier waits for all loads in flight of its warp: 930 cycles for a
+    // warp that fetches rows, measured).
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots]
     uint64_t *p_full = full + kPxSlots;
     uint64_t *q_full = p_full + 1;
-    uint64_t *peer_full = q_full + 1;  // [kPxSlots]
-    uint64_t *peer_p = peer_full + kPxSlots;
-    uint64_t *peer_q = peer_p + 1;
-    uint64_t *empty = peer_q + 1;  // [kPxSlots]
+    uint64_t *empty = q_full + 1;  // [kPxSlots]
     uint64_t *s_full = empty + kPxSlots;  // [2]
     uint64_t *pv_done = s_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 1);
     uint32_t *valid = tmem_slot + 2;  // 16-byte aligned:                          // [4 tiles][8 words] resolved rows
     float *xch = reinterpret_cast<float *>(valid + 32);         // [3][128] maxima of even and odd tiles, sums
     int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 256);   // [64], between the exchanges of sums
-    static_assert(8 * (3 * kPxSlots + 7) + 8 + 128 + 1536 <= kPxMisc && (8 * (3 * kPxSlots + 7) + 8) % 16 == 0, "misc");
+    static_assert(8 * (2 * kPxSlots + 5) + 8 + 128 + 1536 <= kPxMisc && (8 * (2 * kPxSlots + 5) + 8) % 16 == 0, "misc");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
@@ -532,17 +505,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     }
     if (tid == 0) {
         for (int i = 0; i < kPxSlots; ++i) {
-            mbar_init(&full[i], kPxLoadWarps / 2);  // one set
-            mbar_init(&peer_full[i], 1);
+            mbar_init(&full[i], kPxLoadWarps / 2 + (rank == 0));  // one set
             mbar_init(&empty[i], 1);
         }
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(pv_done, 1);
-        mbar_init(p_full, kPxSoftWarps);
-        mbar_init(q_full, kPxSoftWarps);
-        mbar_init(peer_p, 1);
-        mbar_init(peer_q, 1);
+        mbar_init(p_full, kPxSoftWarps + (rank == 0));
+        mbar_init(q_full, kPxSoftWarps + (rank == 0));
         fence_mbar_init();
     }
     tc_fence_before();
@@ -562,6 +532,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     if (warp >= kPxMmaWarp) {
         regs_dec<64>();
         if (n > 0 && warp == kPxMmaWarp && rank == 0 && lane == 0) {
+            // Waits of CTA scope although the second CTA's arrivals count too: this
+            // thread loads none of what they announce, the tensor cores read it
+            // through the async proxy, for which the writers fenced. (A wait that
+            // acquires at cluster scope takes some 250 cycles more, and this thread,
+            // at two a chunk, bounded the kernel: 13,700 cycles a tile.)
             constexpr uint32_t idesc_s = idesc_f16_f32(128, 256, 0, 0), idesc_o = idesc_f16_f32(128, 256, 0, 1);
             const uint64_t a_q = make_sdesc(smem_u32(q_s), 16, 1024, kSw128);
             const uint64_t a_p = make_sdesc(smem_u32(p_s), 16, 1024, kSw128);
@@ -573,13 +548,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             uint32_t chunk = 0, strips = 0;
             bool ok = true;
             auto scores = [&](int i) {
-                if (i == 0 || wk.tile == 0) {
-                    ok = ok && mbar_wait(q_full, strips & 1u) && mbar_wait_cluster(peer_q, strips & 1u);
-                    ++strips;
-                }
+                if (i == 0 || wk.tile == 0) ok = ok && mbar_wait(q_full, strips++ & 1u);
                 for (int d = 0; d < 4 && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u) && mbar_wait_cluster(&peer_full[slot], (chunk / kPxSlots) & 1u);
+                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -597,12 +569,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     wk.next(p);
                     scores(i + 1);
                 }
-                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u) && mbar_wait_cluster(peer_p, (uint32_t)i & 1u);
+                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u);
                 const bool fresh = i == 0 || wv.tile == 0;
                 const int nv = wv.value_chunks();
                 for (int d = 0; d < nv && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u) && mbar_wait_cluster(&peer_full[slot], (chunk / kPxSlots) & 1u);
+                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -624,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             wv = wk;
             uint32_t chunk = 0, strips = 0;
             bool ok = true;
-            const uint32_t to_full = cluster_smem_addr(peer_full, 0), to_p = cluster_smem_addr(peer_p, 0), to_q = cluster_smem_addr(peer_q, 0);
+            const uint32_t to_full = cluster_smem_addr(full, 0), to_p = cluster_smem_addr(p_full, 0), to_q = cluster_smem_addr(q_full, 0);
             auto chunks = [&](int m) {
                 for (int d = 0; d < m && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
