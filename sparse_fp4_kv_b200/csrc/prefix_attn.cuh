@@ -24,8 +24,9 @@
 // CTA holds the keys of half of the tile (128 of the N = 256 columns), for
 // P V all 256 rows of half of the latent width. One CTA alone could not:
 // O of 128 rows fills its TMEM, and of 64 rows costs the tensor pipe as much
-// as 128. N = 256 for both products, because with M = 128 per pair an
-// instruction takes 62 cycles at N = 128 and 64 at N = 256 (measured).
+// as 128. N = 256 for both products: an instruction reads 6 KiB of operands from
+// shared memory in its 64 cycles (N = 128: 4 KiB in 32), which leaves room for
+// the stores of dequantised rows.
 // Shared memory: Q (64 KiB), P (32 KiB) and a ring of four 32 KiB chunks, in
 // the order the products take them: four chunks of 128 latent values of the
 // keys of tile i + 1, then up to four chunks of 64 rows of the values of
@@ -125,8 +126,13 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrives at a barrier of either CTA of the pair. Scope CTA (the default) on
+// purpose: what these barriers announce lies in the arriving CTA's own shared
+// memory, written there and fenced for the async proxy before, and is read by
+// that CTA's tensor core. Releasing at cluster scope took 930 cycles in a warp
+// with loads in flight and bounded the kernel (12,000 cycles a tile).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Registers of the calling group of four warps. The four groups' shares sum up
 // to what the block is launched with (4 x 128): softmax 208, rows 120 each,
@@ -139,6 +145,12 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -480,10 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     uint8_t *p_s = q_s + kPxQBytes;              // [4 blocks of 64 cache rows][64 rows][128 B]
     uint8_t *ring = p_s + kPxPBytes;             // [kPxSlots][32 KiB]
     uint8_t *misc = ring + kPxSlots * kPxSlotBytes;
-    // Barriers at which a CTA's own warps arrive; the last warp of the second CTA
-    // passes its CTA's arrivals on to the first CTA's (an arrival at another
-    // CTA's barrier waits for all loads in flight of its warp: 930 cycles for a
-    // warp that fetches rows, measured).
+    // The first CTA's full, p_full and q_full are what the products wait for:
+    // the warps of both CTAs arrive at them. The others are signalled in both.
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots]
     uint64_t *p_full = full + kPxSlots;
     uint64_t *q_full = p_full + 1;
@@ -505,14 +515,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     }
     if (tid == 0) {
         for (int i = 0; i < kPxSlots; ++i) {
-            mbar_init(&full[i], kPxLoadWarps / 2 + (rank == 0));  // one set
+            mbar_init(&full[i], kPxLoadWarps);  // one set of each CTA
             mbar_init(&empty[i], 1);
         }
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(pv_done, 1);
-        mbar_init(p_full, kPxSoftWarps + (rank == 0));
-        mbar_init(q_full, kPxSoftWarps + (rank == 0));
+        mbar_init(p_full, 2 * kPxSoftWarps);
+        mbar_init(q_full, 2 * kPxSoftWarps);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -531,12 +541,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
 
     if (warp >= kPxMmaWarp) {
         regs_dec<64>();
-        if (n > 0 && warp == kPxMmaWarp && rank == 0 && lane == 0) {
+        if (n > 0 && warp == kPxMmaWarp && rank == 0) {
+            // The whole warp walks and waits, one elected lane issues: descriptors
+            // stay in uniform registers that way (64 cycles an instruction or less;
+            // from a branch of lane 0 alone an instruction took 65 and more to issue,
+            // which bounded the kernel).
             // Waits of CTA scope although the second CTA's arrivals count too: this
-            // thread loads none of what they announce, the tensor cores read it
-            // through the async proxy, for which the writers fenced. (A wait that
-            // acquires at cluster scope takes some 250 cycles more, and this thread,
-            // at two a chunk, bounded the kernel: 13,700 cycles a tile.)
+            // warp loads none of what they announce, the tensor cores read it through
+            // the async proxy, for which the writers fenced. (Acquiring at cluster
+            // scope takes some 250 cycles more a wait.)
             constexpr uint32_t idesc_s = idesc_f16_f32(128, 256, 0, 0), idesc_o = idesc_f16_f32(128, 256, 0, 1);
             const uint64_t a_q = make_sdesc(smem_u32(q_s), 16, 1024, kSw128);
             const uint64_t a_p = make_sdesc(smem_u32(p_s), 16, 1024, kSw128);
@@ -549,19 +562,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             bool ok = true;
             auto scores = [&](int i) {
                 if (i == 0 || wk.tile == 0) ok = ok && mbar_wait(q_full, strips++ & 1u);
+#pragma unroll 1
                 for (int d = 0; d < 4 && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], (chunk / kPxSlots) & 1u));
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t a = a_q + (uint64_t)(d * 16384 >> 4), b = b_k + (uint64_t)(slot * kPxSlotBytes >> 4);
+                    const uint32_t to = tmem + kColS + 128 * (i & 1);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // blocks of 64 values: two of the chunk
-                        mma_f16_pair(tmem + kColS + 128 * (i & 1), a_q + (uint64_t)(((2 * d + (k >> 2)) * 8192 + (k & 3) * 32) >> 4),
-                                     b_k + (uint64_t)((slot * kPxSlotBytes + (k >> 2) * 16384 + (k & 3) * 32) >> 4), idesc_s,
-                                     (d | k) ? 1u : 0u);
-                    tc_commit_pair(&empty[slot]);
+                        for (int k = 0; k < 8; ++k)  // two blocks of 64 values
+                            mma_f16_pair(to, a + (uint64_t)(((k >> 2) * 8192 + (k & 3) * 32) >> 4),
+                                         b + (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4), idesc_s, (d | k) ? 1u : 0u);
+                        tc_commit_pair(&empty[slot]);
+                        if (d == 3) tc_commit_pair(&s_full[i & 1]);
+                    }
+                    __syncwarp();
                 }
-                if (ok) tc_commit_pair(&s_full[i & 1]);
             };
             scores(0);
             for (int i = 0; i < n && ok; ++i) {
@@ -569,57 +587,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     wk.next(p);
                     scores(i + 1);
                 }
-                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u);
-                const bool fresh = i == 0 || wv.tile == 0;
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(p_full, (uint32_t)i & 1u));
+                const uint32_t fresh = i == 0 || wv.tile == 0;
                 const int nv = wv.value_chunks();
+#pragma unroll 1
                 for (int d = 0; d < nv && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], (chunk / kPxSlots) & 1u));
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t a = a_p + (uint64_t)(d * 8192 >> 4), b = b_v + (uint64_t)(slot * kPxSlotBytes >> 4);
+                    const uint32_t add = fresh && d == 0 ? 0u : 1u;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            mma_f16_pair(tmem + 128 * j, a_p + (uint64_t)((d * 8192 + k * 32) >> 4),
-                                         b_v + (uint64_t)((slot * kPxSlotBytes + j * 16384 + k * 2048) >> 4), idesc_o,
-                                         (!fresh || d > 0 || k > 0) ? 1u : 0u);
-                    tc_commit_pair(&empty[slot]);
+                            for (int j = 0; j < 2; ++j)
+                                mma_f16_pair(tmem + 128 * j, a + (uint64_t)(k * 32 >> 4), b + (uint64_t)((j * 16384 + k * 2048) >> 4), idesc_o,
+                                             k > 0 ? 1u : add);
+                        tc_commit_pair(&empty[slot]);
+                        if (d == nv - 1) tc_commit_pair(pv_done);
+                    }
+                    __syncwarp();
                 }
-                if (ok) tc_commit_pair(pv_done);
-                if (i + 1 < n) wv.next(p);
-            }
-        } else if (n > 0 && warp == kPxMmaWarp && rank == 1 && lane == 0) {
-            // the same waits, in the same order, passed on
-            PxWalk wk, wv;
-            wk.begin(p, c, x0);
-            wv = wk;
-            uint32_t chunk = 0, strips = 0;
-            bool ok = true;
-            const uint32_t to_full = cluster_smem_addr(full, 0), to_p = cluster_smem_addr(p_full, 0), to_q = cluster_smem_addr(q_full, 0);
-            auto chunks = [&](int m) {
-                for (int d = 0; d < m && ok; ++d, ++chunk) {
-                    const uint32_t slot = chunk % kPxSlots;
-                    ok = mbar_wait(&full[slot], (chunk / kPxSlots) & 1u);
-                    if (ok) mbar_arrive_cluster(to_full + 8 * slot);
-                }
-            };
-            auto keys = [&](int i) {
-                if (i == 0 || wk.tile == 0) {
-                    ok = ok && mbar_wait(q_full, strips++ & 1u);
-                    if (ok) mbar_arrive_cluster(to_q);
-                }
-                chunks(4);
-            };
-            keys(0);
-            for (int i = 0; i < n && ok; ++i) {
-                if (i + 1 < n) {
-                    wk.next(p);
-                    keys(i + 1);
-                }
-                ok = ok && mbar_wait(p_full, (uint32_t)i & 1u);
-                if (ok) mbar_arrive_cluster(to_p);
-                chunks(wv.value_chunks());
                 if (i + 1 < n) wv.next(p);
             }
         }
@@ -630,6 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // ---- rows of the cache into the ring: two sets of four warps, the first
         // with chunks 0 and 2 of a group of four, the second with 1 and 3 ----
         const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
+        const uint32_t full_addr = cluster_smem_addr(full, 0);
         PxWalk w;
         w.begin(p, c, x0);
         // the rows of a tile that this lane resolves: one of its keys (row 32 lw +
@@ -771,7 +762,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[slot]);
+                    if (lane == 0) mbar_arrive_pair(full_addr + 8 * slot);
                 }
                 if (more) fetch(nxt, d, raw[d]);
             }
@@ -785,6 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // ---- softmax: this thread has row 64 * rank + (tid & 63) of a strip and half of its scores ----
         const int r = tid & 63, half = tid >> 6;
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t p_full_addr = cluster_smem_addr(p_full, 0), q_full_addr = cluster_smem_addr(q_full, 0);
         const int pair_bar = 1 + (warp & 1);  // warps w and w + 2 have the same rows
         PxWalk w;
         w.begin(p, c, x0);
@@ -823,7 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             if (bad) set_error(CSA2_DEVERR_Q_RANGE);
             fence_proxy_async_smem();
             named_bar_sync(3, kPxSoftWarps * 32);  // qrow_s may be written again
-            if (lane == 0) mbar_arrive(q_full);
+            if (lane == 0) mbar_arrive_pair(q_full_addr);
         };
         int32_t q_row, sees, next_q_row = -1, next_sees = 0;
         load_q(w.t, q_row, sees);
@@ -923,7 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) mbar_arrive_pair(p_full_addr);
             if (last) {
                 // the strip's partial of this run
                 xch[256 + tid] = l_run;
