@@ -824,18 +824,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // warps count on this one at their barriers
         for (int i = 0; i < n; ++i) {
             const bool last = i == n - 1 || w.last();
-            PxWalk wn = w;
+            const int lim = min(max(sees - w.tile * kPxTile - 128 * half, 0), 128);
+            // where the strip's partial goes (used when last)
+            const bool pre = w.t.member0 >= 0;
+            const int64_t part = pre ? ((int64_t)c + w.s) * kPxRows + 64 * rank + r : ((int64_t)c + (w.s - w.n_pre)) * p.h + 64 * rank + r;
             if (ok) ok = mbar_wait(&s_full[i & 1], ((uint32_t)i >> 1) & 1u);
             tc_fence_after();
             if (i + 1 < n) {
-                wn.next(p);
+                w.next(p);
                 // Q is free once S of the strip's last tile is done
-                if (last) load_q(wn.t, next_q_row, next_sees);
+                if (last) load_q(w.t, next_q_row, next_sees);
             }
             const uint32_t ts = lane_addr + kColS + 128 * (i & 1);
             // scores of this thread that do not count become -inf, in TMEM and by a
             // loop of its own, so that the common path has no masks
-            const int lim = min(max(sees - w.tile * kPxTile - 128 * half, 0), 128);
             const uint4 vw = *reinterpret_cast<const uint4 *>(valid + (i & 3) * 8 + half * 4);
             if (__any_sync(0xFFFFFFFFu, lim < 128 || (vw.x & vw.y & vw.z & vw.w) != 0xFFFFFFFFu)) {
 #pragma unroll 1
@@ -874,32 +876,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 m_run = top;
                 l_run *= alpha;
             }
-            // P in registers while the products of the tile before still read the last one
             const float at = m_run == -INFINITY ? 0.0f : m_run;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t pk[64];
+            uint32_t pk[32];
+            auto exps = [&](int k0) {  // scores 32 k0 .. + 63
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[32];
-                tmem_ld32(ts + 32 * k, v);
-                tmem_wait_ld();
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[32];
+                    tmem_ld32(ts + 32 * (k0 + k), v);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float a = ex2(fmaf(__uint_as_float(v[2 * j]), p.scale_log2, -at));
-                    const float b = ex2(fmaf(__uint_as_float(v[2 * j + 1]), p.scale_log2, -at));
-                    sum[j & 3] += a + b;
-                    // f16 probabilities: 2^-11 relative, what the products take
-                    const __half2 hh = __floats2half2_rn(a, b);
-                    pk[16 * k + j] = *reinterpret_cast<const uint32_t *>(&hh);
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = ex2(fmaf(__uint_as_float(v[2 * j]), p.scale_log2, -at));
+                        const float b = ex2(fmaf(__uint_as_float(v[2 * j + 1]), p.scale_log2, -at));
+                        sum[j & 3] += a + b;
+                        // f16 probabilities: 2^-11 relative, what the products take
+                        const __half2 hh = __floats2half2_rn(a, b);
+                        pk[16 * k + j] = *reinterpret_cast<const uint32_t *>(&hh);
+                    }
                 }
-            }
-            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            };
+            auto put_p = [&](int blk) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4 *>(p_s + (2 * half + blk) * 8192 + r * 128 + ((x ^ (r & 7)) << 4)) =
+                        make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+            };
+            // half of P in registers while the products of the tile before read the last one
+            exps(0);
             if (i > 0 && ok) ok = mbar_wait(pv_done, (uint32_t)(i - 1) & 1u);
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-                *reinterpret_cast<uint4 *>(p_s + (2 * half + (x >> 3)) * 8192 + r * 128 + (((x & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+            put_p(0);
+            exps(2);
+            put_p(1);
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
 #pragma unroll 1
                 for (int k = 0; k < 256; k += 32) {
@@ -924,10 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (ok) ok = mbar_wait(pv_done, (uint32_t)i & 1u);
                 tc_fence_after();
-                const int row = 64 * rank + r;
-                const bool pre = w.t.member0 >= 0;
-                const int64_t slot = pre ? ((int64_t)c + w.s) * kPxRows + row : ((int64_t)c + (w.s - w.n_pre)) * p.h + row;
-                float *dst = (pre ? p.pre_o : p.own_o) + slot * CSA2_D + 256 * half;
+                float *dst = (pre ? p.pre_o : p.own_o) + part * CSA2_D + 256 * half;
                 const bool mine = ok && q_row >= 0;
 #pragma unroll 1
                 for (int k = 0; k < 256; k += 32) {
@@ -943,14 +950,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     }
                 }
                 if (mine && half == 0)
-                    (pre ? p.pre_lse : p.own_lse)[slot] = l > 0.0f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    (pre ? p.pre_lse : p.own_lse)[part] = l > 0.0f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 tc_fence_before();
                 m_run = -INFINITY;
                 l_run = 0.0f;
                 q_row = next_q_row;
                 sees = next_sees;
             }
-            w = wn;
         }
         }
     }
@@ -959,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     cluster_sync_all();  // no CTA of the pair leaves while the other's products or arrivals reach it
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc2(tmem, 512);
+        tmem_dealloc2(*reinterpret_cast<volatile uint32_t *>(tmem_slot), 512);  // read again: no register across the roles
     }
 }
 
