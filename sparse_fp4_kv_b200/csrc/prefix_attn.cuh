@@ -85,9 +85,9 @@ struct PrefixParams {
 constexpr int kPxTile = 256;  // cache rows of a tile
 constexpr int kPxRows = 128;  // query rows of a strip
 constexpr int kPxSoftWarps = 4;
-constexpr int kPxLoadWarps = 8;
+constexpr int kPxLoadWarps = 16;
 constexpr int kPxMmaWarp = kPxSoftWarps + kPxLoadWarps;
-constexpr int kPxThreads = 16 * 32;  // three idle warps fill the last group of four
+constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;  // three idle warps fill the last group of four
 constexpr int kPxSlots = 4;
 constexpr int kPxSlotBytes = 32768;
 constexpr int kPxQBytes = 64 * CSA2_D * 2;
@@ -96,6 +96,7 @@ constexpr int kPxMisc = 2048;
 constexpr size_t kPxSmem = 1024 + kPxQBytes + kPxPBytes + (size_t)kPxSlots * kPxSlotBytes + kPxMisc;
 constexpr float kPxRescale = 8.0f;  // log2 by which the maximum may rise before O is rescaled
 static_assert(kPxSmem <= 232448, "shared memory of one CTA");
+static_assert(kPxSlots == 4 && kPxLoadWarps == 4 * kPxSlots, "a set of four warps a slot");
 
 // ---------------------------------------------------------------------------
 // cta_group::2 forms and cluster-scope barriers
@@ -134,10 +135,10 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Registers of the calling group of four warps. The four groups' shares sum up
-// to what the block is launched with (4 x 128): softmax 208, rows 120 each,
-// products 64 (with fewer some spill, and a spill is a trip to L2: the carve-out
-// for shared memory leaves little L1).
+// Registers of the calling group of four warps. The six groups' shares sum up to
+// what the block is launched with (6 x 80): softmax 152, rows 4 x 72, products
+// 40. None spills: a spill is a trip to L2, as the carve-out for shared memory
+// leaves little L1.
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -395,6 +396,20 @@ __device__ __forceinline__ int32_t px_row(const PrefixParams &p, const PxLook &x
     return kPxNone;
 }
 
+// What a CTA's resolver warp tells of a tile, up to kPxInfos tiles ahead. Its 256
+// rows are 16 runs of 16: base[g] is the cache row of the run's first row when
+// the run is 16 entries of one page, kPxNone when it holds no row at all, and
+// kPxMixed otherwise (a run across pages, cut off, with window rows or bad
+// pages: the warps that fetch it resolve its rows themselves).
+constexpr int kPxInfos = 4;
+constexpr int32_t kPxMixed = -2;
+struct __align__(16) PxInfo {
+    int32_t base[16];
+    uint32_t valid[8];  // rows there are, a bit each
+    int32_t strip, tile, left;
+    int32_t pad;
+};
+
 // A lane's share of a chunk: four units of 32 values (16 bytes of codes and 2
 // of scales, or 32 bytes of a window row), of rows that are 8 (keys) or 4
 // (values) apart. The lanes of a warp cover whole 64- or 128-byte runs of rows
@@ -415,14 +430,15 @@ __device__ __forceinline__ void px_ld16(uint32_t *v, const void *at, bool take) 
 __device__ __forceinline__ void px_ld4(uint32_t &v, const void *at, bool take) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)take));
 }
-// All four units when their rows lie STEP apart in the cache: at, sc are the
-// first unit's codes and the word that holds its scales.
+// Two units of a run, their rows STEP apart.
 template <int STEP>
-__device__ __forceinline__ void px_fetch_run(const uint8_t *at, const uint8_t *sc, PxRaw &raw, bool take) {
+__device__ __forceinline__ void px_fetch_run(const PrefixParams &p, int64_t row, int d0, PxRaw &raw, int u0) {
+    const uint8_t *at = p.kv.codes + row * (CSA2_D / 2) + d0 / 2;
+    const uint8_t *sc = p.kv.scales + row * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        px_ld16(raw.v[u], at + u * STEP * (CSA2_D / 2), take);
-        px_ld4(raw.sc[u], sc + u * STEP * (CSA2_D / CSA2_BLOCK), take);
+    for (int u = 0; u < 2; ++u) {
+        px_ld16(raw.v[u0 + u], at + u * STEP * (CSA2_D / 2), true);
+        px_ld4(raw.sc[u0 + u], sc + u * STEP * (CSA2_D / CSA2_BLOCK), true);
     }
 }
 // Unit u alone: values d0 .. d0 + 31 of row src. Of a window row's 32 bytes the
@@ -497,14 +513,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // [kPxSlots]
     uint64_t *p_full = full + kPxSlots;
     uint64_t *q_full = p_full + 1;
-    uint64_t *empty = q_full + 1;  // [kPxSlots]
+    uint64_t *empty = q_full + 1;         // [kPxSlots]
     uint64_t *s_full = empty + kPxSlots;  // [2]
     uint64_t *pv_done = s_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 1);
-    uint32_t *valid = tmem_slot + 2;  // 16-byte aligned:                          // [4 tiles][8 words] resolved rows
-    float *xch = reinterpret_cast<float *>(valid + 32);         // [3][128] maxima of even and odd tiles, sums
-    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 256);   // [64], between the exchanges of sums
-    static_assert(8 * (2 * kPxSlots + 5) + 8 + 128 + 1536 <= kPxMisc && (8 * (2 * kPxSlots + 5) + 8) % 16 == 0, "misc");
+    uint64_t *info_full = pv_done + 1;         // [kPxInfos]
+    uint64_t *info_empty = info_full + kPxInfos;  // [kPxInfos]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(info_empty + kPxInfos);
+    PxInfo *infos = reinterpret_cast<PxInfo *>(tmem_slot + 2);   // [kPxInfos]
+    float *xch = reinterpret_cast<float *>(infos + kPxInfos);    // [2][128] maxima of even and odd tiles
+    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 256);    // [64]
+    constexpr int kBars = 2 * kPxSlots + 5 + 2 * kPxInfos;
+    static_assert(8 * kBars + 8 + kPxInfos * sizeof(PxInfo) + 1024 + 256 <= kPxMisc && (8 * kBars + 8) % 16 == 0, "misc");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
@@ -515,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     }
     if (tid == 0) {
         for (int i = 0; i < kPxSlots; ++i) {
-            mbar_init(&full[i], kPxLoadWarps);  // one set of each CTA
+            mbar_init(&full[i], kPxLoadWarps / 2);  // one set of each CTA
             mbar_init(&empty[i], 1);
         }
         mbar_init(&s_full[0], 1);
@@ -523,6 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         mbar_init(pv_done, 1);
         mbar_init(p_full, 2 * kPxSoftWarps);
         mbar_init(q_full, 2 * kPxSoftWarps);
+        for (int i = 0; i < kPxInfos; ++i) {
+            mbar_init(&info_full[i], 1);
+            mbar_init(&info_empty[i], kPxLoadWarps + kPxSoftWarps);
+        }
         fence_mbar_init();
     }
     tc_fence_before();
@@ -540,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     constexpr uint32_t kColS = 256;
 
     if (warp >= kPxMmaWarp) {
-        regs_dec<64>();
+        regs_dec<40>();
         if (n > 0 && warp == kPxMmaWarp && rank == 0) {
             // The whole warp walks and waits, one elected lane issues: descriptors
             // stay in uniform registers that way (64 cycles an instruction or less;
@@ -612,166 +635,161 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 }
                 if (i + 1 < n) wv.next(p);
             }
+        } else if (n > 0 && warp == kPxMmaWarp + 1) {
+            // ---- resolver: lane g has run g of each tile ----
+            PxWalk w;
+            w.begin(p, c, x0);
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const int slot = i % kPxInfos;
+                const int32_t j = w.tile * kPxTile + 16 * (lane & 15);
+                PxLook x;
+                px_look(p, w, 16 * (lane & 15), x);
+                int32_t base = j >= w.t.rows ? kPxNone : kPxMixed;
+                if (j + 16 <= w.t.entries && x.code + 16 <= p.kv.page_size) {
+                    const int64_t row = (int64_t)x.page * p.kv.page_size + x.code;
+                    if (x.page >= 0 && row + 16 <= p.kv.rows_cap) base = (int32_t)row;
+                }
+                uint32_t have = base >= 0 ? 0xFFFFu : 0u;
+                uint32_t mixed = __ballot_sync(0xFFFFFFFFu, base == kPxMixed) & 0xFFFFu;
+                while (mixed) {
+                    const int g = __ffs(mixed) - 1;
+                    mixed &= mixed - 1;
+                    PxLook y;
+                    px_look(p, w, 16 * g + (lane & 15), y);
+                    const uint32_t m = __ballot_sync(0xFFFFFFFFu, px_row(p, y) != kPxNone) & 0xFFFFu;
+                    if ((lane & 15) == g) have = m;
+                }
+                if (i >= kPxInfos) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_empty[slot], (uint32_t)(i / kPxInfos - 1) & 1u));
+                if (!ok) break;
+                PxInfo &f = infos[slot];
+                if (lane < 16) {
+                    f.base[lane] = base;
+                    reinterpret_cast<uint16_t *>(f.valid)[lane] = (uint16_t)have;
+                }
+                if (lane == 0) {
+                    f.strip = w.s;
+                    f.tile = w.tile;
+                    f.left = min(kPxTile, w.t.rows - w.tile * kPxTile);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&info_full[slot]);
+                if (i + 1 < n) w.next(p);
+            }
         }
         __syncwarp();
     } else if (warp >= kPxSoftWarps) {
-        regs_dec<120>();
+        regs_dec<72>();
         if (n > 0) {
-        // ---- rows of the cache into the ring: two sets of four warps, the first
-        // with chunks 0 and 2 of a group of four, the second with 1 and 3 ----
-        const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
-        const uint32_t full_addr = cluster_smem_addr(full, 0);
-        PxWalk w;
-        w.begin(p, c, x0);
-        // the rows of a tile that this lane resolves: one of its keys (row 32 lw +
-        // lane of the CTA's half) and one of its values (row 64 d + 16 lw +
-        // (lane & 15), d = set for the lower lanes, set + 2 for the upper)
-        struct Look {
-            PxLook k, v;
-            int nv;
-            int32_t w_seq;
-        };
-        struct Rows {
-            int32_t k, v;
-            int nv;
-            bool k_run, v_run;  // the warp's 32 keys, its two runs of 16 values lie in a row in the cache
-            const uint8_t *swa;
-        };
-        auto look = [&]() {
-            Look x;
-            px_look(p, w, 128 * rank + 32 * lw + lane, x.k);
-            px_look(p, w, 64 * (2 * (lane >> 4) + set) + 16 * lw + (lane & 15), x.v);
-            x.nv = w.value_chunks();
-            x.w_seq = w.t.w_seq;
-            return x;
-        };
-        auto resolve = [&](int i, const Look &x) {
-            Rows r;
-            r.k = px_row(p, x.k);
-            r.v = px_row(p, x.v);
-            r.nv = x.nv;
-            r.swa = p.swa + (int64_t)x.w_seq * p.swa_seq_stride * CSA2_D;
-            const int32_t k0 = __shfl_sync(0xFFFFFFFFu, r.k, 0), v0 = __shfl_sync(0xFFFFFFFFu, r.v, lane & 16);
-            r.k_run = __all_sync(0xFFFFFFFFu, (int)(r.k >= 0) & (int)(r.k == k0 + lane));
-            r.v_run = __all_sync(0xFFFFFFFFu, (int)(r.v >= 0) & (int)(r.v == v0 + (lane & 15)));
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, r.v != kPxNone);
-            if (lane < 2) reinterpret_cast<uint16_t *>(valid + (i & 3) * 8)[4 * (2 * lane + set) + lw] = (uint16_t)(m >> (16 * lane));
-            return r;
-        };
-        PxRaw raw[2];
-#pragma unroll
-        for (int d = 0; d < 2; ++d)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                raw[d].sc[u] = 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) raw[d].v[u][j] = 0u;
-            }
-        // A group of chunks in hand. One body for both kinds: the loop has to stay
-        // within the instruction cache. Lane l of a warp has
+        // ---- rows of the cache into the ring: four sets of four warps, a slot of
+        // the ring each, so that a set never waits for a phase that another has
+        // yet to begin. Chunk x of the call goes to slot x % 4. Lane l of a warp has
         //   keys: rows 8 u + 4 (l / 8 % 2) + l / 2 % 4 of the warp's 32, units l / 16
         //     (block) and l % 2 of the chunk's 128 values;
-        //   values: rows 4 u + l / 2 % 4 of its 16, units l / 8 and l % 2 of 256.
-        struct Group {
-            int32_t rows;  // this lane's resolved row
-            bool keys, run;
-            int nv;
-            const uint8_t *swa;
-        };
+        //   values: rows 4 u + l / 2 % 4 of its 16, units l / 8 and l % 2 of 256 ----
+        const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
+        const uint32_t full_addr = cluster_smem_addr(&full[set], 0);
         const int k_sub = 4 * ((lane >> 3) & 1) + ((lane >> 1) & 3), v_sub = (lane >> 1) & 3;
-        auto source = [&](const Group &g, int d, int u) {
-            return __shfl_sync(0xFFFFFFFFu, g.rows, g.keys ? 8 * u + k_sub : 16 * d + 4 * u + v_sub);
-        };
-        auto value0 = [&](const Group &g, int d) {  // the first value of the lane's units
-            return (g.keys ? 128 * (2 * d + set) + 64 * (lane >> 4) : 256 * (int)rank + 64 * (lane >> 3)) + 32 * (lane & 1);
-        };
-        auto fetch = [&](const Group &g, int d, PxRaw &x) {
-            const int d0 = value0(g, d);
-            if (g.run) {
-                const int64_t row = (int64_t)__shfl_sync(0xFFFFFFFFu, g.rows, g.keys ? 0 : 16 * d) + (g.keys ? k_sub : v_sub);
-                const uint8_t *at = p.kv.codes + row * (CSA2_D / 2) + d0 / 2;
-                const uint8_t *sc = p.kv.scales + row * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3);
-                const bool take = row >= 0 && row + (g.keys ? 24 : 12) < p.kv.rows_cap;
-                if (g.keys) px_fetch_run<8>(at, sc, x, take);
-                else px_fetch_run<4>(at, sc, x, take);
-                if (!take) set_error(CSA2_DEVERR_SELECT);
-            } else {
+        PxRaw raw;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) px_fetch(p, g.swa, source(g, d, u), d0, x, u);
+        for (int u = 0; u < 4; ++u) {
+            raw.sc[u] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw.v[u][j] = 0u;
+        }
+        // The group whose chunk is in raw. run: whole runs; else rows is what the
+        // lane resolved for the warp (key lane of 32, value lane % 16 of 16).
+        bool keys = true, run = true, skip = false;
+        int d = set;  // which of the group's chunks is the set's
+        int32_t rows = kPxNone;
+        const uint8_t *swa = nullptr;
+        auto value0 = [&]() {
+            return (keys ? 128 * d + 64 * (lane >> 4) : 256 * (int)rank + 64 * (lane >> 3)) + 32 * (lane & 1);
+        };
+        auto source = [&](int u) { return __shfl_sync(0xFFFFFFFFu, rows, keys ? 8 * u + k_sub : 4 * u + v_sub); };
+        // Fetches the set's chunk of tile i's keys or values, a group whose first
+        // chunk is number `first`.
+        auto fetch = [&](int i, bool of_keys, uint32_t first) {
+            const PxInfo &f = infos[i % kPxInfos];
+            keys = of_keys;
+            d = (int)((set - first) & 3u);
+            skip = !keys && 64 * d >= f.left;
+            const int32_t b0 = f.base[keys ? 8 * (int)rank + 2 * lw : 4 * d + lw], b1 = keys ? f.base[8 * (int)rank + 2 * lw + 1] : b0;
+            run = b0 >= 0 && b1 >= 0;
+            const int d0 = value0();
+            if (run) {
+                if (keys) {
+                    px_fetch_run<8>(p, (int64_t)b0 + k_sub, d0, raw, 0);
+                    px_fetch_run<8>(p, (int64_t)b1 + k_sub, d0, raw, 2);
+                } else {
+                    px_fetch_run<4>(p, (int64_t)b0 + v_sub, d0, raw, 0);
+                    px_fetch_run<4>(p, (int64_t)b0 + 8 + v_sub, d0, raw, 2);
+                }
+            } else if (!skip) {
+                PxWalk w;
+                w.n_pre = *p.n_pre;
+                w.s = f.strip;
+                w.tile = f.tile;
+                w.load(p);
+                swa = p.swa + (int64_t)w.t.w_seq * p.swa_seq_stride * CSA2_D;
+                PxLook x;
+                px_look(p, w, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), x);
+                rows = px_row(p, x);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) px_fetch(p, swa, source(u), d0, raw, u);
             }
         };
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[0], 0));
+        uint32_t chunk = 0, round = 0;  // first of the group; the slot's uses so far
+        fetch(0, true, 0);
         // Groups in the order of the products: K(0), K(1), V(0), K(2), V(1), ...,
-        // K(n - 1), V(n - 2), V(n - 1). The rows of a tile are resolved with its
-        // keys; those of the values wait in (q0, q1) for their turn.
-        Rows q0 = resolve(0, look()), q1 = q0;
-        int queued = 1, resolved = 1;
-        Look ahead;
-        auto look_ahead = [&]() {
-            if (resolved < n) {
-                w.next(p);
-                ahead = look();
-            }
-        };
-        look_ahead();
-        Group cur{q0.k, true, q0.k_run, q0.nv, q0.swa};
-        fetch(cur, 0, raw[0]);
-        fetch(cur, 1, raw[1]);
-        uint32_t chunk = 0;  // first of the group
-        bool ok = true;
+        // K(n - 1), V(n - 2), V(n - 1)
 #pragma unroll 1
         for (int j = 0; j < 2 * n && ok; ++j) {
-            const bool more = j + 1 < 2 * n;
-            Group nxt = cur;
-            if ((j & 1) == 0 && j + 2 < 2 * n) {  // K
-                const Rows r = resolve(resolved, ahead);
-                ++resolved;
-                look_ahead();
-                nxt = Group{r.k, true, r.k_run, r.nv, r.swa};
-                if (queued == 0) q0 = r;
-                else q1 = r;
-                ++queued;
-            } else if (more) {  // V
-                nxt = Group{q0.v, false, q0.v_run, q0.nv, q0.swa};
-                q0 = q1;
-                --queued;
-            }
+            const int tile = j == 0 ? 0 : j == 2 * n - 1 ? n - 1 : j & 1 ? (j + 1) / 2 : j / 2 - 1;
+            const int chunks = keys ? 4 : (infos[tile % kPxInfos].left + 63) >> 6;
+            if (!skip) {
+                if (round > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[set], (round - 1) & 1u));
+                if (!ok) break;
+                ++round;
+                // blocks of 64 values: keys [128 rows][128 B], values [64 rows][128 B]
+                uint8_t *s = ring + set * kPxSlotBytes;
+                s += keys ? (lane >> 4) * 16384 + (32 * lw + k_sub) * 128 : (lane >> 3) * 8192 + (16 * lw + v_sub) * 128;
+                const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (keys ? k_sub : v_sub)) << 4;
+                const uint32_t even[4] = {o0, o0 ^ 16u, o0 ^ 32u, o0 ^ 48u};
+                const uint32_t flip = keys ? 0u : 64u;  // rows 4 further on swap the halves of the swizzle
+                const uint32_t odd[4] = {even[0] ^ flip, even[1] ^ flip, even[2] ^ flip, even[3] ^ flip};
+                const int step = keys ? 8 * 128 : 4 * 128;
+                if (run) {
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                if (cur.keys || 2 * d + set < cur.nv) {
-                    const uint32_t at = chunk + 2 * d + set, slot = at % kPxSlots, round = at / kPxSlots;
-                    if (round > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], (round - 1) & 1u));
-                    uint8_t *s = ring + slot * kPxSlotBytes;
-                    if (ok) {
-                        // blocks of 64 values: keys [128 rows][128 B], values [64 rows][128 B]
-                        s += cur.keys ? (lane >> 4) * 16384 + (32 * lw + k_sub) * 128 : (lane >> 3) * 8192 + (16 * lw + v_sub) * 128;
-                        const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (cur.keys ? k_sub : v_sub)) << 4;
-                        const uint32_t even[4] = {o0, o0 ^ 16u, o0 ^ 32u, o0 ^ 48u};
-                        const uint32_t flip = cur.keys ? 0u : 64u;  // rows 4 further on swap the halves of the swizzle
-                        const uint32_t odd[4] = {even[0] ^ flip, even[1] ^ flip, even[2] ^ flip, even[3] ^ flip};
-                        const int step = cur.keys ? 8 * 128 : 4 * 128;
-                        if (cur.run) {
+                    for (int u = 0; u < 4; ++u)
+                        px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? odd : even);
+                } else {
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                px_store_fp4(raw[d].v[u], raw[d].sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? odd : even);
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                px_store(raw[d].v[u], raw[d].sc[u] >> (16 * (lane & 1)), source(cur, d, u), cur.swa + value0(cur, d), s + u * step,
-                                         u & 1 ? odd : even);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(full_addr + 8 * slot);
+                    for (int u = 0; u < 4; ++u)
+                        px_store(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), source(u), swa + value0(), s + u * step, u & 1 ? odd : even);
                 }
-                if (more) fetch(nxt, d, raw[d]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(full_addr);
             }
-            chunk += cur.keys ? 4 : cur.nv;
-            cur = nxt;
+            chunk += chunks;
+            if (!keys) {  // the tile's last use of its info
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&info_empty[tile % kPxInfos]);
+            }
+            if (j + 1 < 2 * n) {
+                const int nj = j + 1;
+                const bool next_keys = (nj & 1) && nj != 2 * n - 1;
+                const int nt = nj == 2 * n - 1 ? n - 1 : nj & 1 ? (nj + 1) / 2 : nj / 2 - 1;
+                if (next_keys) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[nt % kPxInfos], (uint32_t)(nt / kPxInfos) & 1u));
+                if (!ok) break;
+                fetch(nt, next_keys, chunk);
+            }
         }
         }
     } else {
-        regs_inc<208>();
+        regs_inc<152>();
         if (n > 0) {
         // ---- softmax: this thread has row 64 * rank + (tid & 63) of a strip and half of its scores ----
         const int r = tid & 63, half = tid >> 6;
@@ -838,7 +856,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             const uint32_t ts = lane_addr + kColS + 128 * (i & 1);
             // scores of this thread that do not count become -inf, in TMEM and by a
             // loop of its own, so that the common path has no masks
-            const uint4 vw = *reinterpret_cast<const uint4 *>(valid + (i & 3) * 8 + half * 4);
+            const uint4 vw = *reinterpret_cast<const uint4 *>(infos[i % kPxInfos].valid + half * 4);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&info_empty[i % kPxInfos]);
             if (__any_sync(0xFFFFFFFFu, lim < 128 || (vw.x & vw.y & vw.z & vw.w) != 0xFFFFFFFFu)) {
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
@@ -928,9 +948,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             if (lane == 0) mbar_arrive_pair(p_full_addr);
             if (last) {
                 // the strip's partial of this run
-                xch[256 + tid] = l_run;
+                xch[(~i & 1) * 128 + tid] = l_run;
                 named_bar_sync(pair_bar, 64);
-                const float l = l_run + xch[256 + (tid ^ 64)];
+                const float l = l_run + xch[(~i & 1) * 128 + (tid ^ 64)];
+                named_bar_sync(pair_bar, 64);  // the next tile's maxima go there
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (ok) ok = mbar_wait(pv_done, (uint32_t)i & 1u);
                 tc_fence_after();
