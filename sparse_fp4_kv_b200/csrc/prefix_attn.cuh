@@ -412,12 +412,13 @@ struct __align__(16) PxInfo {
 
 // A lane's share of a chunk: four units of 32 values (16 bytes of codes and 2
 // of scales, or 32 bytes of a window row), of rows that are 8 (keys) or 4
-// (values) apart. The lanes of a warp cover whole 64- or 128-byte runs of rows
-// (a lane with a row of its own would touch 32 lines per load: measured, that
-// made the loads the bound), and a quarter warp four rows of one block, so that
-// its 16-byte stores meet the eight bank groups of the swizzle. The loads are
-// predicated instructions on registers that nothing else merges into, so none
-// waits for another.
+// (values) apart. What bounds the kernel is the shared-memory and L1 array: the
+// products' operands (some 3070 cycles a tile), the stores of dequantised rows
+// (2300), and every line that a quarter warp's load touches. So a quarter warp
+// takes whole 64-byte runs of two rows (keys) or 128 bytes of one (values); with
+// four rows of 32 bytes the loads took 3700 cycles of the tile's 9660. The loads
+// are predicated instructions on registers that nothing else merges into, so
+// none waits for another.
 struct PxRaw {
     uint32_t v[4][4], sc[4];
 };
@@ -450,35 +451,50 @@ __device__ __forceinline__ void px_fetch(const PrefixParams &p, const uint8_t *s
     px_ld16(raw.v[u], at, src != kPxNone);
     px_ld4(raw.sc[u], p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3), fp4);
 }
-// A unit of FP4 values dequantised into four 16-byte pieces at dst + off[j].
-// sc: its two scales.
-__device__ __forceinline__ void px_store_fp4(const uint32_t (&raw)[4], uint32_t sc, uint8_t *dst, const uint32_t (&off)[4]) {
+__device__ __forceinline__ void px_swap(uint32_t &a, uint32_t &b, bool yes) {
+    const uint32_t x = yes ? b : a, y = yes ? a : b;
+    a = x;
+    b = y;
+}
+// A unit of FP4 values dequantised into four 16-byte pieces of a swizzled
+// 128-byte row: piece j at dst + (o0 ^ 16 j). The units that a quarter warp
+// stores lie in several blocks; each lane starts with another piece (turn, by
+// block), so that its eight stores meet eight different bank groups. sc: the
+// unit's two scales.
+__device__ __forceinline__ void px_store_fp4(const uint32_t (&raw)[4], uint32_t sc, uint8_t *dst, uint32_t o0, int turn) {
+    uint32_t w[4] = {raw[0], raw[1], raw[2], raw[3]};
     const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)sc);
-    const uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
+    uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
+    px_swap(w[0], w[1], turn & 1);
+    px_swap(w[2], w[3], turn & 1);
+    px_swap(w[0], w[2], turn & 2);
+    px_swap(w[1], w[3], turn & 2);
+    px_swap(f[0], f[1], turn & 2);
+    const uint32_t o = o0 ^ ((uint32_t)turn << 4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t h[4];
-        e2m1x8_to_f16x8(raw[j], h);
-        *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(hmul2_u32(h[0], f[j >> 1]), hmul2_u32(h[1], f[j >> 1]),
-                                                             hmul2_u32(h[2], f[j >> 1]), hmul2_u32(h[3], f[j >> 1]));
+        e2m1x8_to_f16x8(w[j], h);
+        *reinterpret_cast<uint4 *>(dst + (o ^ (j << 4))) = make_uint4(hmul2_u32(h[0], f[j >> 1]), hmul2_u32(h[1], f[j >> 1]),
+                                                                     hmul2_u32(h[2], f[j >> 1]), hmul2_u32(h[3], f[j >> 1]));
     }
 }
 // A unit of any row.
 __device__ __forceinline__ void px_store(const uint32_t (&raw)[4], uint32_t sc, int32_t src, const uint8_t *swa_at, uint8_t *dst,
-                                         const uint32_t (&off)[4]) {
+                                         uint32_t o0, int turn) {
     if (src >= 0) {
-        px_store_fp4(raw, sc, dst, off);
+        px_store_fp4(raw, sc, dst, o0, turn);
     } else if (src != kPxNone) {
         const uint4 m = __ldg(reinterpret_cast<const uint4 *>(swa_at + (int64_t)(-2 - src) * CSA2_D + 16));
         const uint32_t w[8] = {raw[0], raw[1], raw[2], raw[3], m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(
+            *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(
                 e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
                 e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + off[j]) = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -684,12 +700,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // ---- rows of the cache into the ring: four sets of four warps, a slot of
         // the ring each, so that a set never waits for a phase that another has
         // yet to begin. Chunk x of the call goes to slot x % 4. Lane l of a warp has
-        //   keys: rows 8 u + 4 (l / 8 % 2) + l / 2 % 4 of the warp's 32, units l / 16
-        //     (block) and l % 2 of the chunk's 128 values;
-        //   values: rows 4 u + l / 2 % 4 of its 16, units l / 8 and l % 2 of 256 ----
+        //   keys: rows 8 u + l / 4 of the warp's 32, unit l % 4 of the chunk's 128
+        //     values;
+        //   values: rows 4 u + l / 8 of its 16, unit l % 8 of 256 ----
         const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
         const uint32_t full_addr = cluster_smem_addr(&full[set], 0);
-        const int k_sub = 4 * ((lane >> 3) & 1) + ((lane >> 1) & 3), v_sub = (lane >> 1) & 3;
+        const int k_sub = lane >> 2, v_sub = lane >> 3;
         PxRaw raw;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -704,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         int32_t rows = kPxNone;
         const uint8_t *swa = nullptr;
         auto value0 = [&]() {
-            return (keys ? 128 * d + 64 * (lane >> 4) : 256 * (int)rank + 64 * (lane >> 3)) + 32 * (lane & 1);
+            return keys ? 128 * d + 32 * (lane & 3) : 256 * (int)rank + 32 * (lane & 7);
         };
         auto source = [&](int u) { return __shfl_sync(0xFFFFFFFFu, rows, keys ? 8 * u + k_sub : 4 * u + v_sub); };
         // Fetches the set's chunk of tile i's keys or values, a group whose first
@@ -754,20 +770,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 ++round;
                 // blocks of 64 values: keys [128 rows][128 B], values [64 rows][128 B]
                 uint8_t *s = ring + set * kPxSlotBytes;
-                s += keys ? (lane >> 4) * 16384 + (32 * lw + k_sub) * 128 : (lane >> 3) * 8192 + (16 * lw + v_sub) * 128;
+                const int blk = (lane >> 1) & (keys ? 1 : 3), turn = keys ? 2 * blk : blk;
+                s += keys ? blk * 16384 + (32 * lw + k_sub) * 128 : blk * 8192 + (16 * lw + v_sub) * 128;
                 const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (keys ? k_sub : v_sub)) << 4;
-                const uint32_t even[4] = {o0, o0 ^ 16u, o0 ^ 32u, o0 ^ 48u};
-                const uint32_t flip = keys ? 0u : 64u;  // rows 4 further on swap the halves of the swizzle
-                const uint32_t odd[4] = {even[0] ^ flip, even[1] ^ flip, even[2] ^ flip, even[3] ^ flip};
+                const uint32_t o1 = keys ? o0 : o0 ^ 64u;  // rows 4 further on swap the halves of the swizzle
                 const int step = keys ? 8 * 128 : 4 * 128;
                 if (run) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? odd : even);
+                        px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? o1 : o0, turn);
                 } else {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        px_store(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), source(u), swa + value0(), s + u * step, u & 1 ? odd : even);
+                        px_store(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), source(u), swa + value0(), s + u * step, u & 1 ? o1 : o0, turn);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
