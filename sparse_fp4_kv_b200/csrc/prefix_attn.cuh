@@ -373,17 +373,18 @@ constexpr int32_t kPxNone = -1;
 struct PxLook {
     int32_t code, page;
 };
-__device__ __forceinline__ void px_look(const PrefixParams &p, const PxWalk &w, int r, PxLook &x) {
-    const int32_t j = w.tile * kPxTile + r;
+template <class T>  // a strip or what an info tells of one
+__device__ __forceinline__ void px_look(const PrefixParams &p, const T &strip, int32_t tile, int r, PxLook &x) {
+    const int32_t j = tile * kPxTile + r;
     x.code = kPxNone;
     x.page = -1;
-    if (j < w.t.entries) {
-        const uint32_t t = (uint32_t)w.t.t_base + (uint32_t)j;  // below max_pages * page_size (px_limit)
+    if (j < strip.entries) {
+        const uint32_t t = (uint32_t)strip.t_base + (uint32_t)j;  // below max_pages * page_size (px_limit)
         const uint32_t page = t / (uint32_t)p.kv.page_size;
         x.code = (int32_t)(t - page * (uint32_t)p.kv.page_size);
-        x.page = p.kv.page_table[(int64_t)w.t.seq * p.kv.max_pages + page];
-    } else if (j < w.t.rows) {
-        int64_t sl = (int64_t)w.t.w_begin + (j - w.t.entries);  // below twice the stride
+        x.page = p.kv.page_table[(int64_t)strip.seq * p.kv.max_pages + page];
+    } else if (j < strip.rows) {
+        int64_t sl = (int64_t)strip.w_begin + (j - strip.entries);  // below twice the stride
         if (sl >= p.swa_seq_stride) sl -= p.swa_seq_stride;
         x.code = -2 - (int32_t)sl;
     }
@@ -398,16 +399,17 @@ __device__ __forceinline__ int32_t px_row(const PrefixParams &p, const PxLook &x
 
 // What a CTA's resolver warp tells of a tile, up to kPxInfos tiles ahead. Its 256
 // rows are 16 runs of 16: base[g] is the cache row of the run's first row when
-// the run is 16 entries of one page, kPxNone when it holds no row at all, and
-// kPxMixed otherwise (a run across pages, cut off, with window rows or bad
-// pages: the warps that fetch it resolve its rows themselves).
+// the run is 16 entries of one page, kPxWindow - slot when it is 16 rows of the
+// window ring from that slot on, kPxNone when it holds no row at all, and
+// kPxMixed otherwise (a run across pages, cut off, both entries and window, or
+// with bad pages: the warps that fetch it resolve its rows themselves).
 constexpr int kPxInfos = 4;
-constexpr int32_t kPxMixed = -2;
+constexpr int32_t kPxMixed = -2, kPxWindow = -3;
 struct __align__(16) PxInfo {
     int32_t base[16];
     uint32_t valid[8];  // rows there are, a bit each
-    int32_t strip, tile, left;
-    int32_t pad;
+    int32_t tile, left;
+    int32_t seq, t_base, entries, rows, w_begin, w_seq;  // as in the strip
 };
 
 // A lane's share of a chunk: four units of 32 values (16 bytes of codes and 2
@@ -479,23 +481,36 @@ __device__ __forceinline__ void px_store_fp4(const uint32_t (&raw)[4], uint32_t 
                                                                      hmul2_u32(h[2], f[j >> 1]), hmul2_u32(h[3], f[j >> 1]));
     }
 }
+// A unit of a window row (raw: its first 16 bytes).
+__device__ __forceinline__ void px_store_e4m3(const uint32_t (&raw)[4], const uint4 &m, uint8_t *dst, uint32_t o0) {
+    const uint32_t w[8] = {raw[0], raw[1], raw[2], raw[3], m.x, m.y, m.z, m.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(
+            e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
+            e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
+}
 // A unit of any row.
 __device__ __forceinline__ void px_store(const uint32_t (&raw)[4], uint32_t sc, int32_t src, const uint8_t *swa_at, uint8_t *dst,
                                          uint32_t o0, int turn) {
     if (src >= 0) {
         px_store_fp4(raw, sc, dst, o0, turn);
     } else if (src != kPxNone) {
-        const uint4 m = __ldg(reinterpret_cast<const uint4 *>(swa_at + (int64_t)(-2 - src) * CSA2_D + 16));
-        const uint32_t w[8] = {raw[0], raw[1], raw[2], raw[3], m.x, m.y, m.z, m.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(
-                e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
-                e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
+        px_store_e4m3(raw, __ldg(reinterpret_cast<const uint4 *>(swa_at + (int64_t)(-2 - src) * CSA2_D + 16)), dst, o0);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(0u, 0u, 0u, 0u);
     }
+}
+
+// Eight f32 values times f as one 32-byte store (whole sectors: a thread of the
+// epilogue has a row of its own).
+__device__ __forceinline__ void px_st32(float *dst, const uint32_t *v, float f) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(__uint_as_float(v[0]) * f),
+                 "f"(__uint_as_float(v[1]) * f), "f"(__uint_as_float(v[2]) * f), "f"(__uint_as_float(v[3]) * f),
+                 "f"(__uint_as_float(v[4]) * f), "f"(__uint_as_float(v[5]) * f), "f"(__uint_as_float(v[6]) * f),
+                 "f"(__uint_as_float(v[7]) * f)
+                 : "memory");
 }
 
 // Row of q (query * h + head) of row r of a strip and the entries it sees of
@@ -660,19 +675,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 const int slot = i % kPxInfos;
                 const int32_t j = w.tile * kPxTile + 16 * (lane & 15);
                 PxLook x;
-                px_look(p, w, 16 * (lane & 15), x);
+                px_look(p, w.t, w.tile, 16 * (lane & 15), x);
                 int32_t base = j >= w.t.rows ? kPxNone : kPxMixed;
+                if (j >= w.t.entries && j + 16 <= w.t.rows && (int64_t)(-2 - x.code) + 16 <= p.swa_seq_stride) base = kPxWindow + 2 + x.code;
                 if (j + 16 <= w.t.entries && x.code + 16 <= p.kv.page_size) {
                     const int64_t row = (int64_t)x.page * p.kv.page_size + x.code;
                     if (x.page >= 0 && row + 16 <= p.kv.rows_cap) base = (int32_t)row;
                 }
-                uint32_t have = base >= 0 ? 0xFFFFu : 0u;
+                uint32_t have = base >= 0 || base <= kPxWindow ? 0xFFFFu : 0u;
                 uint32_t mixed = __ballot_sync(0xFFFFFFFFu, base == kPxMixed) & 0xFFFFu;
                 while (mixed) {
                     const int g = __ffs(mixed) - 1;
                     mixed &= mixed - 1;
                     PxLook y;
-                    px_look(p, w, 16 * g + (lane & 15), y);
+                    px_look(p, w.t, w.tile, 16 * g + (lane & 15), y);
                     const uint32_t m = __ballot_sync(0xFFFFFFFFu, px_row(p, y) != kPxNone) & 0xFFFFu;
                     if ((lane & 15) == g) have = m;
                 }
@@ -684,13 +700,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     reinterpret_cast<uint16_t *>(f.valid)[lane] = (uint16_t)have;
                 }
                 if (lane == 0) {
-                    f.strip = w.s;
                     f.tile = w.tile;
                     f.left = min(kPxTile, w.t.rows - w.tile * kPxTile);
+                    f.seq = w.t.seq;
+                    f.t_base = w.t.t_base;
+                    f.entries = w.t.entries;
+                    f.rows = w.t.rows;
+                    f.w_begin = w.t.w_begin;
+                    f.w_seq = w.t.w_seq;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&info_full[slot]);
-                if (i + 1 < n) w.next(p);
+                if (i + 1 < n) {
+                    w.next(p);
+                    if (w.tile == 0 && w.t.member0 < 0) {
+                        // q of a strip of one query lies together: into L2 before its turn
+                        const int m = min(64, w.t.q_rows - 64 * (int)rank);  // this CTA's rows
+                        const uint8_t *q = reinterpret_cast<const uint8_t *>(p.q + ((int64_t)w.t.row0 + 64 * rank) * CSA2_D);
+                        for (int o = lane * 128; o < m * CSA2_D * 2; o += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
+                    }
+                }
             }
         }
         __syncwarp();
@@ -713,12 +742,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
 #pragma unroll
             for (int j = 0; j < 4; ++j) raw.v[u][j] = 0u;
         }
-        // The group whose chunk is in raw. run: whole runs; else rows is what the
-        // lane resolved for the warp (key lane of 32, value lane % 16 of 16).
-        bool keys = true, run = true, skip = false;
+        // The group whose chunk is in raw. Entries or window rows in whole runs, or
+        // else rows: what the lane resolved for the warp (key lane of 32, value lane
+        // % 16 of 16).
+        enum { kRunEntries, kRunWindow, kRows } kind = kRunEntries;
+        bool keys = true, skip = false;
         int d = set;  // which of the group's chunks is the set's
         int32_t rows = kPxNone;
-        const uint8_t *swa = nullptr;
+        const uint8_t *swa = nullptr;  // the window's ring; a run of window rows: at the lane's first unit
         auto value0 = [&]() {
             return keys ? 128 * d + 32 * (lane & 3) : 256 * (int)rank + 32 * (lane & 7);
         };
@@ -731,9 +762,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             d = (int)((set - first) & 3u);
             skip = !keys && 64 * d >= f.left;
             const int32_t b0 = f.base[keys ? 8 * (int)rank + 2 * lw : 4 * d + lw], b1 = keys ? f.base[8 * (int)rank + 2 * lw + 1] : b0;
-            run = b0 >= 0 && b1 >= 0;
+            kind = b0 >= 0 && b1 >= 0 ? kRunEntries : b0 <= kPxWindow && (keys ? b1 == b0 - 16 : true) ? kRunWindow : kRows;
             const int d0 = value0();
-            if (run) {
+            if (kind == kRunEntries) {
                 if (keys) {
                     px_fetch_run<8>(p, (int64_t)b0 + k_sub, d0, raw, 0);
                     px_fetch_run<8>(p, (int64_t)b1 + k_sub, d0, raw, 2);
@@ -742,17 +773,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     px_fetch_run<4>(p, (int64_t)b0 + 8 + v_sub, d0, raw, 2);
                 }
             } else if (!skip) {
-                PxWalk w;
-                w.n_pre = *p.n_pre;
-                w.s = f.strip;
-                w.tile = f.tile;
-                w.load(p);
-                swa = p.swa + (int64_t)w.t.w_seq * p.swa_seq_stride * CSA2_D;
-                PxLook x;
-                px_look(p, w, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), x);
-                rows = px_row(p, x);
+                swa = p.swa + (int64_t)f.w_seq * p.swa_seq_stride * CSA2_D;
+                if (kind == kRunWindow) {
+                    swa += (int64_t)(kPxWindow - b0 + (keys ? k_sub : v_sub)) * CSA2_D + d0;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) px_fetch(p, swa, source(u), d0, raw, u);
+                    for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], swa + u * (keys ? 8 : 4) * CSA2_D, true);
+                } else {
+                    PxLook x;
+                    px_look(p, f, f.tile, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), x);
+                    rows = px_row(p, x);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) px_fetch(p, swa, source(u), d0, raw, u);
+                }
             }
         };
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[0], 0));
@@ -775,10 +807,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (keys ? k_sub : v_sub)) << 4;
                 const uint32_t o1 = keys ? o0 : o0 ^ 64u;  // rows 4 further on swap the halves of the swizzle
                 const int step = keys ? 8 * 128 : 4 * 128;
-                if (run) {
+                if (kind == kRunEntries) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? o1 : o0, turn);
+                } else if (kind == kRunWindow) {
+                    // the second halves of the units, of sectors that the first ones brought
+#pragma unroll
+                    for (int v = 0; v < 4; v += 2) {
+                        uint4 m[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) m[u] = __ldg(reinterpret_cast<const uint4 *>(swa + (v + u) * (keys ? 8 : 4) * CSA2_D + 16));
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) px_store_e4m3(raw.v[v + u], m[u], s + (v + u) * step, u & 1 ? o1 : o0);
+                    }
                 } else {
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
@@ -820,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             if (half == 0) qrow_s[r] = q_row;
             named_bar_sync(3, kPxSoftWarps * 32);
             bool bad = false;
-            constexpr int kBatch = 8;
+            constexpr int kBatch = 16;
 #pragma unroll 1
             for (int k0 = 0; k0 < 32; k0 += kBatch) {
                 uint4 v[kBatch];
@@ -973,16 +1015,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 float *dst = (pre ? p.pre_o : p.own_o) + part * CSA2_D + 256 * half;
                 const bool mine = ok && q_row >= 0;
 #pragma unroll 1
-                for (int k = 0; k < 256; k += 32) {
-                    uint32_t v[32];
+                for (int k = 0; k < 256; k += 64) {
+                    uint32_t v[32], y[32];
                     tmem_ld32(lane_addr + k, v);
+                    tmem_ld32(lane_addr + k + 32, y);
                     tmem_wait_ld();
                     if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(dst + k + j) =
-                                make_float4(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv,
-                                            __uint_as_float(v[j + 2]) * inv, __uint_as_float(v[j + 3]) * inv);
+                        for (int j = 0; j < 32; j += 8) px_st32(dst + k + j, v + j, inv);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) px_st32(dst + k + 32 + j, y + j, inv);
                     }
                 }
                 if (mine && half == 0)
