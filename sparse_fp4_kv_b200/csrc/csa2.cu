@@ -1445,7 +1445,7 @@ unsigned copy_blocks(int64_t rows) {
 constexpr int64_t kPxMaxQueries = 1 << 17;
 struct PrefixLayout {
     int32_t pairs, max_pre;
-    size_t off_start, off_mgroup, off_gstrip, off_gtiles, off_strips, off_pre_o, off_pre_lse, off_own_o, off_own_lse, total;
+    size_t off_start, off_start_tile, off_mgroup, off_gstrip, off_gtiles, off_strips, off_q16, off_pre_o, off_pre_lse, off_own_o, off_own_lse, total;
 };
 PrefixLayout prefix_layout(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h) {
     PrefixLayout L{};
@@ -1459,16 +1459,31 @@ PrefixLayout prefix_layout(int32_t n_members, int32_t n_groups, int32_t q_per_se
         return at;
     };
     L.off_start = take((size_t)L.pairs * 4);
+    L.off_start_tile = take((size_t)(L.pairs + 1) * 8);
     L.off_mgroup = take((size_t)n_members * 4);
     L.off_gstrip = take((size_t)n_groups * 4);
     L.off_gtiles = take((size_t)n_groups * 8);
     L.off_strips = take((size_t)(L.max_pre + n_own) * sizeof(PrefixStrip));
+    L.off_q16 = take((size_t)n_own * h * CSA2_D * 2);
     L.off_pre_o = take((size_t)(L.pairs + L.max_pre) * kPxRows * CSA2_D * 4);
     L.off_pre_lse = take((size_t)(L.pairs + L.max_pre) * kPxRows * 4);
     L.off_own_o = take((size_t)(L.pairs + n_own) * h * CSA2_D * 4);
     L.off_own_lse = take((size_t)(L.pairs + n_own) * h * 4);
     L.total = off;
     return L;
+}
+
+// q in f16 [rows][512] as boxes of 64 values by 64 rows with the 128B swizzle;
+// rows behind the last read as zeros.
+bool make_q_map(CUtensorMap *tm, uint16_t *q16, int64_t rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {CSA2_D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {CSA2_D * 2};
+    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q16, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Pairs of CTAs of the attention kernel that the current device runs at once
@@ -1660,13 +1675,15 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     p.n_groups = n_groups;
     uint8_t *b = static_cast<uint8_t *>(ws);
     p.total_tiles = reinterpret_cast<int64_t *>(b);
-    p.n_pre = reinterpret_cast<int32_t *>(b + 8);
+    p.n_pre = reinterpret_cast<int32_t *>(b + 16);
     p.start = reinterpret_cast<int32_t *>(b + L.off_start);
+    p.start_tile = reinterpret_cast<int64_t *>(b + L.off_start_tile);
     p.member_group = reinterpret_cast<int32_t *>(b + L.off_mgroup);
     p.group_strip = reinterpret_cast<int32_t *>(b + L.off_gstrip);
     p.group_tiles = reinterpret_cast<int64_t *>(b + L.off_gtiles);
     p.strips = reinterpret_cast<PrefixStrip *>(b + L.off_strips);
     p.max_pre = L.max_pre;
+    p.q16 = reinterpret_cast<uint16_t *>(b + L.off_q16);
     p.pre_o = reinterpret_cast<float *>(b + L.off_pre_o);
     p.pre_lse = reinterpret_cast<float *>(b + L.off_pre_lse);
     p.own_o = reinterpret_cast<float *>(b + L.off_own_o);
@@ -1675,9 +1692,14 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     // a second wave of pairs would double the time of equal runs
     p.pairs = std::min(L.pairs, prefix_resident_pairs());
     if (p.pairs < 1) return CSA2_ERR_CUDA;
-    launch(k_prefix_plan, dim3(1), dim3(kPxPlanThreads), 0, stream, p);
+    const int64_t q_rows = (int64_t)n_members * q_per_seq * h;
+    CUtensorMap q_map;
+    if (!make_q_map(&q_map, p.q16, q_rows)) return CSA2_ERR_CUDA;
+    // block 0 plans, the others convert q (64 threads a row)
+    const int64_t conv = std::min<int64_t>(2 * num_sms() - 1, (q_rows * (CSA2_D / 8) + kPxPlanThreads - 1) / kPxPlanThreads);
+    launch(k_prefix_plan, dim3(1 + (unsigned)conv), dim3(kPxPlanThreads), 0, stream, p);
     if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
-    launch(k_prefix_attn, dim3(2 * (unsigned)p.pairs), dim3(kPxThreads), kPxSmem, stream, p);
+    launch(k_prefix_attn, dim3(2 * (unsigned)p.pairs), dim3(kPxThreads), kPxSmem, stream, q_map, p);
     if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
     launch(k_prefix_merge, dim3((unsigned)(n_members * q_per_seq), (unsigned)h), dim3(kPxMergeThreads), 0, stream, p);
     return check_launch();

@@ -44,6 +44,7 @@ namespace csa2 {
 // One strip: rows of queries against a list of cache rows.
 struct __align__(16) PrefixStrip {
     int64_t tile0;     // first tile in the call's list
+    int64_t cost0;     // the same in the list's costs (see px_lo)
     int32_t ntiles;    // tiles of 256 rows (0: nothing to attend)
     int32_t rows;      // length of the list of cache rows
     int32_t seq;       // page-table row of its entries
@@ -52,7 +53,8 @@ struct __align__(16) PrefixStrip {
     int32_t w_begin;   // ring slot of the first window row
     int32_t q_rows;    // rows of queries, at most 128
     int32_t member0;   // prefix: first member of the group; own: -1
-    int32_t row0;      // prefix: first row among the group's (member, query, head) rows; own: query * h
+    int32_t row0;      // prefix: first row among the group's (member, query, head) rows; own: 0
+    int32_t q_at;      // first row in q16
     int32_t w_seq;     // sequence of the window
 };
 
@@ -70,14 +72,16 @@ struct PrefixParams {
     uint32_t q_flip;   // sign bits of two f16 values when the softmax scale is negative
     int32_t nq, q_per_seq, h, w_max, n_members, n_groups, pairs;
     // workspace
-    int64_t *total_tiles;   // [1]
+    int64_t *total_tiles;   // [2] tiles, and their cost with the strips'
     int32_t *n_pre;         // [1] prefix strips
     int32_t *start;         // [pairs] first strip of each pair's run
+    int64_t *start_tile;    // [pairs + 1] first tile of each run
     int32_t *member_group;  // [n_members], -1: not computed
     int32_t *group_strip;   // [n_groups] first strip of a group
     int64_t *group_tiles;   // [n_groups] tiles of one strip of a group
     PrefixStrip *strips;    // [max_pre + n_members * q_per_seq], the prefix strips first
     int32_t max_pre;
+    uint16_t *q16;          // [n_members * q_per_seq * h][512] q in f16, in the order of members
     float *pre_o, *pre_lse;  // [pairs + max_pre][128][512], [..][128]
     float *own_o, *own_lse;  // [pairs + n_members * q_per_seq][h][512], [..][h]
 };
@@ -160,14 +164,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// the split of the tile list over the pairs: no more pairs than tiles, so that
-// every run has a tile and a strip's partials are those of consecutive pairs
+// the split of the tile list over the pairs: equal shares of a cost of one per
+// tile and kPxStripCost per strip (loading its q, filling the pipeline and
+// storing its partial). No more pairs than tiles, so that a strip's partials are
+// those of consecutive pairs.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t total) { return (int32_t)min((int64_t)pairs, total); }
-__device__ __forceinline__ int64_t px_lo(int64_t total, int32_t pairs, int64_t c) { return c * total / pairs; }
-// the pair whose run holds tile x
-__device__ __forceinline__ int32_t px_owner(int64_t total, int32_t pairs, int64_t x) {
-    return (int32_t)(((x + 1) * pairs - 1) / total);
+constexpr int kPxStripCost = 1;
+__device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t tiles) { return (int32_t)min((int64_t)pairs, tiles); }
+__device__ __forceinline__ int64_t px_lo(int64_t cost, int32_t pairs, int64_t c) { return c * cost / pairs; }
+// the pair whose share holds tile x of strip t
+__device__ __forceinline__ int32_t px_owner(int64_t cost, int32_t pairs, const PrefixStrip &t, int32_t x) {
+    return (int32_t)(((t.cost0 + kPxStripCost + x + 1) * pairs - 1) / cost);
 }
 
 // Visible entries of query u of sequence s.
@@ -209,19 +216,51 @@ __device__ __forceinline__ int64_t px_block_exclusive(int64_t v, int64_t *warp_s
     return before;
 }
 
+// q in f16 (the sign turned for a negative scale), rows in the order of members:
+// the rows of a strip then lie together and one tiled copy a block of 64 values
+// brings them into shared memory, swizzled. 16 bytes a thread.
+__device__ __forceinline__ void px_convert_q(const PrefixParams &p, int64_t rows) {
+    const int64_t step = (int64_t)(gridDim.x - 1) * kPxPlanThreads;
+    bool bad = false;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * kPxPlanThreads + threadIdx.x; i < rows * (CSA2_D / 8); i += step) {
+        const int32_t row = (int32_t)(i / (CSA2_D / 8)), c = (int32_t)(i % (CSA2_D / 8));
+        const int32_t per = p.q_per_seq * p.h, j = row / per, y = row - j * per;
+        const int32_t seq = p.members[j];
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (seq >= 0 && seq < p.kv.batch) {
+            const int64_t u = (int64_t)seq * p.q_per_seq + y / p.h;
+            if (u < p.nq) v = __ldg(reinterpret_cast<const uint4 *>(p.q + (u * p.h + y % p.h) * CSA2_D) + c);
+        }
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // 65536 and more (0x4780 and up, infinities and NaN too) have no finite f16 value
+            bad |= (w[k] & 0x7FFFu) >= 0x4780u || ((w[k] >> 16) & 0x7FFFu) >= 0x4780u;
+            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            o[k] = *reinterpret_cast<const uint32_t *>(&h) ^ p.q_flip;
+        }
+        reinterpret_cast<uint4 *>(p.q16)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (bad) set_error(CSA2_DEVERR_Q_RANGE);
+}
+
 __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) {
     __shared__ int64_t sums[32];
     __shared__ int32_t descends;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
+    const int32_t n_own = p.n_members * p.q_per_seq, ps_rows = p.q_per_seq * p.h;
+    if (blockIdx.x > 0) {
+        px_convert_q(p, (int64_t)n_own * p.h);
+        return;
+    }
     if (tid == 0) descends = 0;
     __syncthreads();
-    const int32_t n_own = p.n_members * p.q_per_seq, ps_rows = p.q_per_seq * p.h;
     for (int32_t g = tid; g < p.n_groups; g += kPxPlanThreads)
         if (p.group_begin[g] > p.group_begin[g + 1]) descends = 1;
     for (int32_t j = tid; j < p.n_members; j += kPxPlanThreads) p.member_group[j] = -1;
-    for (int32_t c = tid; c < p.pairs; c += kPxPlanThreads) p.start[c] = 0;
     __syncthreads();
     // groups that overlap could not be told apart: a list that descends is refused as a whole
     const bool all_bad = descends != 0;
@@ -259,7 +298,7 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
                     }
                 }
                 PrefixStrip t;
-                t.tile0 = 0;
+                t.tile0 = t.cost0 = 0;
                 t.entries = max(0, limit - prefix);
                 t.rows = t.entries + nw;
                 t.ntiles = (int32_t)(((int64_t)t.rows + kPxTile - 1) / kPxTile);
@@ -268,7 +307,8 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
                 t.w_begin = wb;
                 t.q_rows = p.h;
                 t.member0 = -1;
-                t.row0 = (int32_t)u * p.h;
+                t.row0 = 0;
+                t.q_at = i * p.h;
                 t.w_seq = s;
                 own[i] = t;
             }
@@ -281,7 +321,7 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
     }
     __syncthreads();
     // prefix strips: where each group's start, and their tiles
-    int64_t strips = 0, tiles = 0;
+    int64_t strips = 0, tiles = 0, cost = 0;
     for (int32_t g0 = 0; g0 < p.n_groups; g0 += kPxPlanThreads) {
         const int32_t g = g0 + tid;
         int32_t n = 0, nt = 0, seen = 0, b0 = 0, rows = 0;
@@ -295,10 +335,12 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
         int64_t ts, tt;
         const int64_t s0 = strips + px_block_exclusive(n, sums, ts);
         const int64_t t0 = tiles + px_block_exclusive((int64_t)n * nt, sums, tt);
+        const int64_t c0 = t0 + kPxStripCost * s0;  // every prefix strip has tiles
         if (g < p.n_groups) p.group_strip[g] = n ? (int32_t)s0 : -1;
         for (int32_t x = 0; x < n && s0 + x < p.max_pre; ++x) {
             PrefixStrip t;
             t.tile0 = t0 + (int64_t)x * nt;
+            t.cost0 = c0 + (int64_t)x * (nt + kPxStripCost);
             t.ntiles = nt;
             t.rows = seen;
             t.seq = p.members[b0];
@@ -308,6 +350,7 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
             t.q_rows = min(kPxRows, rows - x * kPxRows);
             t.member0 = b0;
             t.row0 = x * kPxRows;
+            t.q_at = b0 * ps_rows + x * kPxRows;
             t.w_seq = 0;
             p.strips[s0 + x] = t;
         }
@@ -315,27 +358,39 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
         tiles += tt;
     }
     const int32_t n_pre = (int32_t)strips;
+    cost = tiles + kPxStripCost * strips;
     for (int32_t i0 = 0; i0 < n_own; i0 += kPxPlanThreads) {
         const int32_t i = i0 + tid;
         int64_t tt;
-        const int64_t t0 = tiles + px_block_exclusive(i < n_own ? own[i].ntiles : 0, sums, tt);
-        if (i < n_own) own[i].tile0 = t0;
+        const int32_t nt = i < n_own ? own[i].ntiles : 0;
+        const int64_t t0 = tiles + px_block_exclusive(nt, sums, tt);
+        int64_t cc;
+        const int64_t c0 = cost + px_block_exclusive(nt ? nt + kPxStripCost : 0, sums, cc);
+        if (i < n_own) {
+            own[i].tile0 = t0;
+            own[i].cost0 = c0;
+        }
         tiles += tt;
+        cost += cc;
     }
+    const int32_t pairs = px_pairs(p.pairs, tiles);
     if (tid == 0) {
-        *p.total_tiles = tiles;
+        p.total_tiles[0] = tiles;
+        p.total_tiles[1] = cost;
         *p.n_pre = n_pre;
+        p.start_tile[pairs] = tiles;
     }
     if (tiles == 0) return;
-    // the first strip of every pair's run
-    const int32_t pairs = px_pairs(p.pairs, tiles);
+    // where each pair's share begins: its first strip and tile
     for (int32_t i = tid; i < n_pre + n_own; i += kPxPlanThreads) {
         const PrefixStrip &t = i < n_pre ? p.strips[i] : own[i - n_pre];
         if (t.ntiles == 0) continue;
-        // pairs c with tile0 <= lo(c) < tile0 + ntiles
-        const int64_t t1 = t.tile0 + t.ntiles;
-        for (int64_t c = (t.tile0 * pairs + tiles - 1) / tiles; c < pairs && px_lo(tiles, pairs, c) < t1; ++c)
+        // pairs c with cost0 <= lo(c) < cost0 + kPxStripCost + ntiles
+        const int64_t end = t.cost0 + kPxStripCost + t.ntiles;
+        for (int64_t c = (t.cost0 * pairs + cost - 1) / cost; c < pairs && px_lo(cost, pairs, c) < end; ++c) {
             p.start[c] = i;
+            p.start_tile[c] = t.tile0 + max((int64_t)0, px_lo(cost, pairs, c) - t.cost0 - kPxStripCost);
+        }
     }
 }
 
@@ -503,36 +558,20 @@ __device__ __forceinline__ void px_store(const uint32_t (&raw)[4], uint32_t sc, 
     }
 }
 
-// Eight f32 values times f as one 32-byte store (whole sectors: a thread of the
-// epilogue has a row of its own).
-__device__ __forceinline__ void px_st32(float *dst, const uint32_t *v, float f) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(__uint_as_float(v[0]) * f),
-                 "f"(__uint_as_float(v[1]) * f), "f"(__uint_as_float(v[2]) * f), "f"(__uint_as_float(v[3]) * f),
-                 "f"(__uint_as_float(v[4]) * f), "f"(__uint_as_float(v[5]) * f), "f"(__uint_as_float(v[6]) * f),
-                 "f"(__uint_as_float(v[7]) * f)
-                 : "memory");
-}
-
-// Row of q (query * h + head) of row r of a strip and the entries it sees of
-// the strip's list; -1 where there is none.
-__device__ __forceinline__ int32_t px_q_row(const PrefixParams &p, const PrefixStrip &t, int r, int32_t &sees) {
-    sees = 0;
+// Entries that row r of a strip sees of the strip's list; -1 where there is no
+// such row.
+__device__ __forceinline__ int32_t px_sees(const PrefixParams &p, const PrefixStrip &t, int r) {
     if (r >= t.q_rows) return -1;
-    if (t.member0 < 0) {
-        sees = t.rows;
-        return t.row0 + r;
-    }
+    if (t.member0 < 0) return t.rows;
     const int32_t x = t.row0 + r, per = p.q_per_seq * p.h;
     const int32_t j = x / per, y = x - j * per;
     const int32_t s = p.members[t.member0 + j];
     if (s < 0 || s >= p.kv.batch) return -1;
     const int64_t u = (int64_t)s * p.q_per_seq + y / p.h;
-    if (u >= p.nq) return -1;
-    sees = min(px_limit(p, s, u), t.rows);
-    return (int32_t)u * p.h + y % p.h;
+    return u < p.nq ? min(px_limit(p, s, u), t.rows) : -1;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_prefix_attn(PrefixParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_prefix_attn(const __grid_constant__ CUtensorMap q_map, PrefixParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *q_s = base;                         // [8 blocks of 64 values][64 rows][128 B]
@@ -549,12 +588,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     uint64_t *pv_done = s_full + 2;
     uint64_t *info_full = pv_done + 1;         // [kPxInfos]
     uint64_t *info_empty = info_full + kPxInfos;  // [kPxInfos]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(info_empty + kPxInfos);
+    uint64_t *q_copy = info_empty + kPxInfos;     // [2], the second unused
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_copy + 2);
     PxInfo *infos = reinterpret_cast<PxInfo *>(tmem_slot + 2);   // [kPxInfos]
     float *xch = reinterpret_cast<float *>(infos + kPxInfos);    // [2][128] maxima of even and odd tiles
-    int32_t *qrow_s = reinterpret_cast<int32_t *>(xch + 256);    // [64]
-    constexpr int kBars = 2 * kPxSlots + 5 + 2 * kPxInfos;
-    static_assert(8 * kBars + 8 + kPxInfos * sizeof(PxInfo) + 1024 + 256 <= kPxMisc && (8 * kBars + 8) % 16 == 0, "misc");
+    constexpr int kBars = 2 * kPxSlots + 5 + 2 * kPxInfos + 2;
+    static_assert(8 * kBars + 8 + kPxInfos * sizeof(PxInfo) + 1024 <= kPxMisc && (8 * kBars + 8) % 16 == 0, "misc");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
@@ -572,7 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         mbar_init(&s_full[1], 1);
         mbar_init(pv_done, 1);
         mbar_init(p_full, 2 * kPxSoftWarps);
-        mbar_init(q_full, 2 * kPxSoftWarps);
+        mbar_init(q_full, 2);
+        mbar_init(q_copy, 1);
         for (int i = 0; i < kPxInfos; ++i) {
             mbar_init(&info_full[i], 1);
             mbar_init(&info_empty[i], kPxLoadWarps + kPxSoftWarps);
@@ -587,10 +627,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     pdl_wait();
 
     const int32_t c = blockIdx.x >> 1;
-    const int64_t total = *p.total_tiles;
-    const int32_t pairs = px_pairs(p.pairs, total);
-    const int64_t x0 = c < pairs ? px_lo(total, pairs, c) : 0;
-    const int n = c < pairs ? (int)(px_lo(total, pairs, c + 1) - x0) : 0;
+    const int32_t pairs = px_pairs(p.pairs, *p.total_tiles);
+    const int64_t x0 = c < pairs ? p.start_tile[c] : 0;
+    const int n = c < pairs ? (int)(p.start_tile[c + 1] - x0) : 0;
     constexpr uint32_t kColS = 256;
 
     if (warp >= kPxMmaWarp) {
@@ -711,15 +750,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&info_full[slot]);
-                if (i + 1 < n) {
-                    w.next(p);
-                    if (w.tile == 0 && w.t.member0 < 0) {
-                        // q of a strip of one query lies together: into L2 before its turn
-                        const int m = min(64, w.t.q_rows - 64 * (int)rank);  // this CTA's rows
-                        const uint8_t *q = reinterpret_cast<const uint8_t *>(p.q + ((int64_t)w.t.row0 + 64 * rank) * CSA2_D);
-                        for (int o = lane * 128; o < m * CSA2_D * 2; o += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
+                if (i + 1 < n) w.next(p);
+            }
+        } else if (n > 0 && warp == kPxMmaWarp + 2) {
+            // ---- q of each strip, once S of the last tile before is done ----
+            const uint32_t q_full_addr = cluster_smem_addr(q_full, 0);
+            PxWalk w;
+            w.begin(p, c, x0);
+            bool ok = true;
+            uint32_t copies = 0;
+            for (int i = 0; i < n && ok; ++i) {
+                if (i == 0 || w.tile == 0) {
+                    if (w.t.q_rows > 64 * (int)rank) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_copy, kPxQBytes);
+                            for (int b = 0; b < 8; ++b) tma_load_2d(q_s + b * 8192, &q_map, q_copy, 64 * b, w.t.q_at + 64 * (int)rank);
+                        }
+                        __syncwarp();
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_copy, copies & 1u));
+                        ++copies;
                     }
+                    if (ok && lane == 0) mbar_arrive_pair(q_full_addr);
                 }
+                // every phase of s_full is waited for, so that none is mistaken for another
+                if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[i & 1], ((uint32_t)i >> 1) & 1u));
+                if (i + 1 < n) w.next(p);
             }
         }
         __syncwarp();
@@ -851,49 +906,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // ---- softmax: this thread has row 64 * rank + (tid & 63) of a strip and half of its scores ----
         const int r = tid & 63, half = tid >> 6;
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t p_full_addr = cluster_smem_addr(p_full, 0), q_full_addr = cluster_smem_addr(q_full, 0);
+        const uint32_t p_full_addr = cluster_smem_addr(p_full, 0);
         const int pair_bar = 1 + (warp & 1);  // warps w and w + 2 have the same rows
         PxWalk w;
         w.begin(p, c, x0);
         bool ok = true;
-        // Q of a strip into shared memory (f16): the barrier tells the products
-        auto load_q = [&](const PrefixStrip &t, int32_t &q_row, int32_t &sees) {
-            q_row = px_q_row(p, t, 64 * rank + r, sees);
-            if (half == 0) qrow_s[r] = q_row;
-            named_bar_sync(3, kPxSoftWarps * 32);
-            bool bad = false;
-            constexpr int kBatch = 16;
-#pragma unroll 1
-            for (int k0 = 0; k0 < 32; k0 += kBatch) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int32_t src = qrow_s[2 * (k0 + k) + half];
-                    v[k] = src >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)src * CSA2_D) + (tid & 63)) : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int row = 2 * (k0 + k) + half, c64 = tid & 63;
-                    const uint32_t w4[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    uint32_t o4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // 65536 and more (0x4780 and up, infinities and NaN too) have no finite f16 value
-                        bad |= (w4[j] & 0x7FFFu) >= 0x4780u || ((w4[j] >> 16) & 0x7FFFu) >= 0x4780u;
-                        const __half2 hh = __floats2half2_rn(__uint_as_float(w4[j] << 16), __uint_as_float(w4[j] & 0xFFFF0000u));
-                        o4[j] = *reinterpret_cast<const uint32_t *>(&hh) ^ p.q_flip;
-                    }
-                    *reinterpret_cast<uint4 *>(q_s + (c64 >> 3) * 8192 + row * 128 + (((c64 & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                }
-            }
-            if (bad) set_error(CSA2_DEVERR_Q_RANGE);
-            fence_proxy_async_smem();
-            named_bar_sync(3, kPxSoftWarps * 32);  // qrow_s may be written again
-            if (lane == 0) mbar_arrive_pair(q_full_addr);
-        };
-        int32_t q_row, sees, next_q_row = -1, next_sees = 0;
-        load_q(w.t, q_row, sees);
+        int32_t sees = px_sees(p, w.t, 64 * rank + r), next_sees = -1;
         float m_run = -INFINITY, l_run = 0.0f;
         // after a wait that gave up the loop goes on without waiting: the other
         // warps count on this one at their barriers
@@ -907,8 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             tc_fence_after();
             if (i + 1 < n) {
                 w.next(p);
-                // Q is free once S of the strip's last tile is done
-                if (last) load_q(w.t, next_q_row, next_sees);
+                if (last) next_sees = px_sees(p, w.t, 64 * rank + r);
             }
             const uint32_t ts = lane_addr + kColS + 128 * (i & 1);
             // scores of this thread that do not count become -inf, in TMEM and by a
@@ -1012,28 +1029,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (ok) ok = mbar_wait(pv_done, (uint32_t)i & 1u);
                 tc_fence_after();
-                float *dst = (pre ? p.pre_o : p.own_o) + part * CSA2_D + 256 * half;
-                const bool mine = ok && q_row >= 0;
+                // O / l through the P buffer (free now), 64 columns at a time: a thread
+                // has 256 bytes of its row there, in 16-byte units turned by its lane;
+                // half a warp then stores a row's 256 bytes
+                const bool mine = ok && sees >= 0;
+                const uint32_t whose = __ballot_sync(0xFFFFFFFFu, mine);
+                uint8_t *stage = p_s + warp * 8192;
+                float *dst = (pre ? p.pre_o : p.own_o) + (part - lane) * CSA2_D + 256 * half;
 #pragma unroll 1
                 for (int k = 0; k < 256; k += 64) {
-                    uint32_t v[32], y[32];
-                    tmem_ld32(lane_addr + k, v);
-                    tmem_ld32(lane_addr + k + 32, y);
-                    tmem_wait_ld();
-                    if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) px_st32(dst + k + j, v + j, inv);
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t v[32];
+                        tmem_ld32(lane_addr + k + 32 * y, v);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) px_st32(dst + k + 32 + j, y + j, inv);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(stage + lane * 256 + (((8 * y + j) ^ (lane & 15)) << 4)) =
+                                make_float4(__uint_as_float(v[4 * j]) * inv, __uint_as_float(v[4 * j + 1]) * inv,
+                                            __uint_as_float(v[4 * j + 2]) * inv, __uint_as_float(v[4 * j + 3]) * inv);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int row = 2 * j + (lane >> 4);
+                        const float4 o = *reinterpret_cast<const float4 *>(stage + row * 256 + (((lane ^ row) & 15) << 4));
+                        if (whose >> row & 1u) *(reinterpret_cast<float4 *>(dst + (int64_t)row * CSA2_D + k) + (lane & 15)) = o;
+                    }
+                    __syncwarp();
                 }
                 if (mine && half == 0)
                     (pre ? p.pre_lse : p.own_lse)[part] = l > 0.0f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 tc_fence_before();
                 m_run = -INFINITY;
                 l_run = 0.0f;
-                q_row = next_q_row;
                 sees = next_sees;
+                named_bar_sync(3, kPxSoftWarps * 32);  // P may be written again
             }
         }
         }
@@ -1066,8 +1097,8 @@ __global__ void __launch_bounds__(kPxMergeThreads) k_prefix_merge(PrefixParams p
     if (g < 0) return;
     const int64_t u = (int64_t)p.members[j] * p.q_per_seq + qi;
     if (u >= p.nq) return;
-    const int64_t total = *p.total_tiles;
-    const int32_t pairs = px_pairs(p.pairs, total);
+    const int64_t cost = p.total_tiles[1];
+    const int32_t pairs = px_pairs(p.pairs, p.total_tiles[0]);
     int32_t na = 0, nb = 0;
     int64_t a0 = 0, b0 = 0;  // first rows of the partials
     const int32_t s0 = p.group_strip[g];
@@ -1075,14 +1106,14 @@ __global__ void __launch_bounds__(kPxMergeThreads) k_prefix_merge(PrefixParams p
         const int32_t x = ((j - p.group_begin[g]) * p.q_per_seq + qi) * p.h + head;
         const int32_t s = s0 + x / kPxRows;
         const PrefixStrip t = p.strips[s];
-        const int32_t c = px_owner(total, pairs, t.tile0);
-        na = px_owner(total, pairs, t.tile0 + t.ntiles - 1) - c + 1;
+        const int32_t c = px_owner(cost, pairs, t, 0);
+        na = px_owner(cost, pairs, t, t.ntiles - 1) - c + 1;
         a0 = ((int64_t)c + s) * kPxRows + x % kPxRows;
     }
     const PrefixStrip t = p.strips[p.max_pre + i];
     if (t.ntiles > 0) {
-        const int32_t c = px_owner(total, pairs, t.tile0);
-        nb = px_owner(total, pairs, t.tile0 + t.ntiles - 1) - c + 1;
+        const int32_t c = px_owner(cost, pairs, t, 0);
+        nb = px_owner(cost, pairs, t, t.ntiles - 1) - c + 1;
         b0 = ((int64_t)c + i) * p.h + head;
     }
     const int32_t np = na + nb;
