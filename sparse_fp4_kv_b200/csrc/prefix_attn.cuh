@@ -169,7 +169,7 @@ __device__ __forceinline__ float ex2(float x) {
 // storing its partial). No more pairs than tiles, so that a strip's partials are
 // those of consecutive pairs.
 // ---------------------------------------------------------------------------
-constexpr int kPxStripCost = 1;
+constexpr int kPxStripCost = 2;
 __device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t tiles) { return (int32_t)min((int64_t)pairs, tiles); }
 __device__ __forceinline__ int64_t px_lo(int64_t cost, int32_t pairs, int64_t c) { return c * cost / pairs; }
 // the pair whose share holds tile x of strip t
@@ -499,15 +499,6 @@ __device__ __forceinline__ void px_fetch_run(const PrefixParams &p, int64_t row,
         px_ld4(raw.sc[u0 + u], sc + u * STEP * (CSA2_D / CSA2_BLOCK), true);
     }
 }
-// Unit u alone: values d0 .. d0 + 31 of row src. Of a window row's 32 bytes the
-// first 16 are fetched; the rest, of the same sector, when the unit is stored
-// (window rows are few, and registers limit the fetching warps).
-__device__ __forceinline__ void px_fetch(const PrefixParams &p, const uint8_t *swa_seq, int32_t src, int d0, PxRaw &raw, int u) {
-    const bool fp4 = src >= 0;
-    const uint8_t *at = fp4 ? p.kv.codes + (int64_t)src * (CSA2_D / 2) + d0 / 2 : swa_seq + (int64_t)(-2 - src) * CSA2_D + d0;
-    px_ld16(raw.v[u], at, src != kPxNone);
-    px_ld4(raw.sc[u], p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3), fp4);
-}
 __device__ __forceinline__ void px_swap(uint32_t &a, uint32_t &b, bool yes) {
     const uint32_t x = yes ? b : a, y = yes ? a : b;
     a = x;
@@ -545,19 +536,6 @@ __device__ __forceinline__ void px_store_e4m3(const uint32_t (&raw)[4], const ui
             e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
             e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
 }
-// A unit of any row.
-__device__ __forceinline__ void px_store(const uint32_t (&raw)[4], uint32_t sc, int32_t src, const uint8_t *swa_at, uint8_t *dst,
-                                         uint32_t o0, int turn) {
-    if (src >= 0) {
-        px_store_fp4(raw, sc, dst, o0, turn);
-    } else if (src != kPxNone) {
-        px_store_e4m3(raw, __ldg(reinterpret_cast<const uint4 *>(swa_at + (int64_t)(-2 - src) * CSA2_D + 16)), dst, o0);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(0u, 0u, 0u, 0u);
-    }
-}
-
 // Entries that row r of a strip sees of the strip's list; -1 where there is no
 // such row.
 __device__ __forceinline__ int32_t px_sees(const PrefixParams &p, const PrefixStrip &t, int r) {
@@ -837,8 +815,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     PxLook x;
                     px_look(p, f, f.tile, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), x);
                     rows = px_row(p, x);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) px_fetch(p, swa, source(u), d0, raw, u);
                 }
             }
         };
@@ -876,10 +852,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
 #pragma unroll
                         for (int u = 0; u < 2; ++u) px_store_e4m3(raw.v[v + u], m[u], s + (v + u) * step, u & 1 ? o1 : o0);
                     }
-                } else {
+                } else {  // few chunks: loaded only here, unit by unit, which spares registers
+                    const int d0 = value0();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        px_store(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), source(u), swa + value0(), s + u * step, u & 1 ? o1 : o0, turn);
+                    for (int u = 0; u < 4; ++u) {
+                        const int32_t src = source(u);
+                        uint8_t *to = s + u * step;
+                        const uint32_t o = u & 1 ? o1 : o0;
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (src >= 0) {
+                            v = __ldg(reinterpret_cast<const uint4 *>(p.kv.codes + (int64_t)src * (CSA2_D / 2) + d0 / 2));
+                            const uint16_t sc = __ldg(reinterpret_cast<const uint16_t *>(p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + d0 / CSA2_BLOCK));
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            px_store_fp4(w, sc, to, o, turn);
+                        } else if (src != kPxNone) {
+                            const uint8_t *at = swa + (int64_t)(-2 - src) * CSA2_D + d0;
+                            v = __ldg(reinterpret_cast<const uint4 *>(at));
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            px_store_e4m3(w, __ldg(reinterpret_cast<const uint4 *>(at + 16)), to, o);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + (o ^ (k << 4))) = v;
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
