@@ -775,18 +775,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
 #pragma unroll
             for (int j = 0; j < 4; ++j) raw.v[u][j] = 0u;
         }
-        // The group whose chunk is in raw. Entries or window rows in whole runs, or
-        // else rows: what the lane resolved for the warp (key lane of 32, value lane
-        // % 16 of 16).
+        // The group whose chunk is in raw: entries or window rows in whole runs, or
+        // rows that are resolved and loaded when the chunk is stored. What else the
+        // later steps need of its tile they read again from its info.
         enum { kRunEntries, kRunWindow, kRows } kind = kRunEntries;
         bool keys = true, skip = false;
         int d = set;  // which of the group's chunks is the set's
-        int32_t rows = kPxNone;
-        const uint8_t *swa = nullptr;  // the window's ring; a run of window rows: at the lane's first unit
         auto value0 = [&]() {
             return keys ? 128 * d + 32 * (lane & 3) : 256 * (int)rank + 32 * (lane & 7);
         };
-        auto source = [&](int u) { return __shfl_sync(0xFFFFFFFFu, rows, keys ? 8 * u + k_sub : 4 * u + v_sub); };
+        // The window ring of a tile; of a run of window rows, the lane's first unit.
+        auto ring_of = [&](const PxInfo &f) { return p.swa + (int64_t)f.w_seq * p.swa_seq_stride * CSA2_D; };
+        auto run_of = [&](const PxInfo &f) {
+            const int32_t b0 = f.base[keys ? 8 * (int)rank + 2 * lw : 4 * d + lw];
+            return ring_of(f) + (int64_t)(kPxWindow - b0 + (keys ? k_sub : v_sub)) * CSA2_D + value0();
+        };
         // Fetches the set's chunk of tile i's keys or values, a group whose first
         // chunk is number `first`.
         auto fetch = [&](int i, bool of_keys, uint32_t first) {
@@ -805,17 +808,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     px_fetch_run<4>(p, (int64_t)b0 + v_sub, d0, raw, 0);
                     px_fetch_run<4>(p, (int64_t)b0 + 8 + v_sub, d0, raw, 2);
                 }
-            } else if (!skip) {
-                swa = p.swa + (int64_t)f.w_seq * p.swa_seq_stride * CSA2_D;
-                if (kind == kRunWindow) {
-                    swa += (int64_t)(kPxWindow - b0 + (keys ? k_sub : v_sub)) * CSA2_D + d0;
+            } else if (kind == kRunWindow && !skip) {
+                const uint8_t *at = run_of(f);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], swa + u * (keys ? 8 : 4) * CSA2_D, true);
-                } else {
-                    PxLook x;
-                    px_look(p, f, f.tile, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), x);
-                    rows = px_row(p, x);
-                }
+                for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], at + u * (keys ? 8 : 4) * CSA2_D, true);
             }
         };
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[0], 0));
@@ -844,19 +840,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                         px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? o1 : o0, turn);
                 } else if (kind == kRunWindow) {
                     // the second halves of the units, of sectors that the first ones brought
+                    const uint8_t *at = run_of(infos[tile % kPxInfos]) + 16;
 #pragma unroll
                     for (int v = 0; v < 4; v += 2) {
                         uint4 m[2];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) m[u] = __ldg(reinterpret_cast<const uint4 *>(swa + (v + u) * (keys ? 8 : 4) * CSA2_D + 16));
+                        for (int u = 0; u < 2; ++u) m[u] = __ldg(reinterpret_cast<const uint4 *>(at + (v + u) * (keys ? 8 : 4) * CSA2_D));
 #pragma unroll
                         for (int u = 0; u < 2; ++u) px_store_e4m3(raw.v[v + u], m[u], s + (v + u) * step, u & 1 ? o1 : o0);
                     }
-                } else {  // few chunks: loaded only here, unit by unit, which spares registers
+                } else {  // few chunks: resolved (a row a lane) and loaded only here, which spares registers
+                    const PxInfo &f = infos[tile % kPxInfos];
+                    PxLook look;
+                    px_look(p, f, f.tile, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), look);
+                    const int32_t rows = px_row(p, look);
                     const int d0 = value0();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const int32_t src = source(u);
+                        const int32_t src = __shfl_sync(0xFFFFFFFFu, rows, keys ? 8 * u + k_sub : 4 * u + v_sub);
                         uint8_t *to = s + u * step;
                         const uint32_t o = u & 1 ? o1 : o0;
                         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -866,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                             px_store_fp4(w, sc, to, o, turn);
                         } else if (src != kPxNone) {
-                            const uint8_t *at = swa + (int64_t)(-2 - src) * CSA2_D + d0;
+                            const uint8_t *at = ring_of(f) + (int64_t)(-2 - src) * CSA2_D + d0;
                             v = __ldg(reinterpret_cast<const uint4 *>(at));
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                             px_store_e4m3(w, __ldg(reinterpret_cast<const uint4 *>(at + 16)), to, o);
