@@ -107,7 +107,11 @@ __device__ __forceinline__ int4 plan_refs(const int32_t *refs, int32_t p, int32_
     return make_int4(p < hi ? refs[p] : -1, p + 1 < hi ? refs[p + 1] : -1, p + 2 < hi ? refs[p + 2] : -1, p + 3 < hi ? refs[p + 3] : -1);
 }
 
-// Sum of `mine` over the cluster's CTAs before this one, and over all.
+// The two halves of cluster_sync_all().
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// Sum of a count over the cluster's CTAs before this one, and over all.
 __device__ __forceinline__ void cluster_sums(PlanShared &sh, int which, uint32_t rank, int32_t &before, int32_t &all) {
     before = all = 0;
     for (uint32_t c = 0; c < kPlanCtas; ++c) {
@@ -161,21 +165,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
     const uint32_t rank = cluster_rank();
     pdl_trigger();
     pdl_wait();
-    for (int32_t b = rank * kPlanThreads + threadIdx.x; b < p.kv.batch; b += kPlanCtas * kPlanThreads)
-        p.claim[b] = INT32_MAX;
-    const int32_t run = ((p.num_pages + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
-    const int32_t lo = min((int64_t)p.num_pages, (int64_t)rank * run), hi = min((int64_t)p.num_pages, (int64_t)lo + run);
-    const int32_t rounds = (hi - lo + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    int32_t mine = 0;
-    for (int32_t k = 0; k < rounds; ++k) {
-        const int4 r = plan_refs(p.refs, plan_page(lo, k), hi);
-        mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    }
-    int32_t total;
-    block_exclusive(mine, sh.warp_sums, total);
-    if (threadIdx.x == 0) sh.count[0] = total;
-    cluster_sync_all();  // the claims are cleared, the counts in place
-    if (rank == 0) {
+    if (rank == 0) {  // the entries, while the other CTAs count
+        for (int32_t b = threadIdx.x; b < p.kv.batch; b += kPlanThreads) p.claim[b] = INT32_MAX;
+        __syncthreads();
         for (int32_t i = threadIdx.x; i < p.n; i += kPlanThreads) {
             const int32_t s = p.to[i];
             if (s >= 0 && s < p.kv.batch) atomicMin(p.claim + s, i);
@@ -195,10 +187,22 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
         }
         if (threadIdx.x == 0) sh.total_need = (int32_t)min(sum, (int64_t)p.num_pages);
     }
+    const int32_t run = ((p.num_pages + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
+    const int32_t lo = min((int64_t)p.num_pages, (int64_t)rank * run), hi = min((int64_t)p.num_pages, (int64_t)lo + run);
+    const int32_t rounds = (hi - lo + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    int32_t mine = 0;
+    for (int32_t k = 0; k < rounds; ++k) {
+        const int4 r = plan_refs(p.refs, plan_page(lo, k), hi);
+        mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+    }
+    int32_t total;
+    block_exclusive(mine, sh.warp_sums, total);
+    if (threadIdx.x == 0) sh.count[0] = total;
     cluster_sync_all();
     int32_t before, all;
     cluster_sums(sh, 0, rank, before, all);
     const int32_t need = min(cluster_peer(&sh, 0)->total_need, all);
+    cluster_arrive();  // done with the other CTAs' shared memory
     if (rank == 0 && threadIdx.x == 0) {
         p.head[0] = all;
         p.head[1] = need;
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
             }
         before += t;
     }
-    cluster_sync_all();  // no CTA leaves while another reads its shared memory
+    cluster_wait();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------------------
