@@ -1523,12 +1523,18 @@ int32_t prefix_resident_pairs() {
     return n;
 }
 
+// Whether the plan's cluster applies as well: up to kFuseCells table cells and
+// kFuseRows rows to move, eight of each for a thread or a warp of the cluster.
+constexpr int64_t kFuseCells = 8 * kPlanCtas * kPlanThreads, kFuseRows = 8 * kPlanCtas * (kPlanThreads / 32) * kCopyUnitRows;
+
 template <bool FORK>
 csa2_status pages_run(PagesParams &p, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const csa2_status st = pages_workspace(p, ws, ws_bytes);
     if (st != CSA2_OK) return st;
+    p.fused = (int64_t)p.n * p.kv.max_pages <= kFuseCells && (int64_t)p.n * p.kv.page_size <= kFuseRows;
     launch_cluster(k_pages_plan<FORK>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream, kPlanCtas, p);
     if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
+    if (p.fused) return CSA2_OK;
     // along x: enough blocks for the longest row at four columns a thread and
     // for a page copy, but no more than fill the machine with all entries
     const int64_t cols = ((int64_t)p.kv.max_pages + 4 * kApplyThreads - 1) / (4 * kApplyThreads);

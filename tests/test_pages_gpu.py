@@ -146,7 +146,7 @@ def test_no_pages_left_in_the_order_of_the_entries(B, cuda_device):
         g.same(pool, PAGES if pool.refused else 0)
 
 
-@pytest.mark.parametrize("ps,di,seed", [(32, 64, 0), (64, 128, 1), (128, 0, 2), (64, 64, 3)])
+@pytest.mark.parametrize("ps,di,seed", [(32, 64, 0), (64, 128, 1), (128, 0, 2), (64, 64, 3), (4096, 64, 4)])
 def test_random_turns(B, cuda_device, ps, di, seed):
     """Forks, growth, rollbacks into shared pages, frees and compactions in turn."""
     rng = np.random.default_rng(seed)
