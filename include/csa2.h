@@ -374,13 +374,15 @@ size_t csa2_pages_workspace_size(int32_t n, int32_t batch, int64_t num_pages);
  *   sees nothing gets o = 0, lse = -inf; o and lse of sequences in no group
  *   stay as they were. h in 1 ... CSA2_PREFIX_MAX_HEADS.
  * An entry outside the page table or the cache is left out and sets
- * CSA2_DEVERR_BAD_ROW, and so do a limit beyond the row of the page table
- * (cut), a member outside the batch (skipped), a group that does not lie
+ * CSA2_DEVERR_BAD_ROW, and so do a limit beyond the row of the page table or
+ * 2^30 (cut), a member outside the batch (skipped), a group that does not lie
  * within members (skipped), a group_begin that descends anywhere (nothing is
  * computed) and a bad window (dropped). A sequence is to be listed once: o of
- * one listed twice may be that of either place. Arithmetic and the range of q
- * are those of csa2_sparse_attn_decode. n_groups = 0 is a no-op; at most 2^17
- * queries (n_members * q_per_seq).
+ * one listed twice may be that of either place. The scales of entries that a
+ * query of the group sees have to be finite, as csa2_append_fp4 writes them.
+ * Arithmetic and the range of q are those of csa2_sparse_attn_decode. n_groups
+ * = 0 is a no-op; at most 2^17 queries (n_members * q_per_seq), w_max and
+ * swa_seq_stride below 2^30.
  * ws: at least csa2_prefix_attn_workspace_size(n_members, n_groups,
  * q_per_seq, h) bytes, whatever the lengths.
  */

@@ -1661,6 +1661,7 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     if (has_swa && (!swa || !swa_end || swa_seq_stride <= 0 || !aligned(swa, 16) || !aligned(swa_begin, 4) || !aligned(swa_end, 4)))
         return CSA2_ERR_INVALID_ARG;
     if (!has_swa && w_max > 0) return CSA2_ERR_INVALID_ARG;
+    if (has_swa && (w_max >= kPxMostRows || swa_seq_stride >= kPxMostRows)) return CSA2_ERR_UNSUPPORTED;
     const PrefixLayout L = prefix_layout(n_members, n_groups, q_per_seq, h);
     if (!ws || ws_bytes < L.total || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
     PrefixParams p{};

@@ -177,9 +177,11 @@ __device__ __forceinline__ int32_t px_owner(int64_t cost, int32_t pairs, const P
     return (int32_t)(((t.cost0 + kPxStripCost + x + 1) * pairs - 1) / cost);
 }
 
-// Visible entries of query u of sequence s.
+// Visible entries of query u of sequence s: at most what a row of the page table
+// holds and 2^30, so that a list of entries and window rows stays below 2^31.
+constexpr int32_t kPxMostRows = 1 << 30;
 __device__ __forceinline__ int32_t px_limit(const PrefixParams &p, int32_t s, int64_t u) {
-    const int64_t room = (int64_t)p.kv.max_pages * p.kv.page_size;
+    const int64_t room = min((int64_t)p.kv.max_pages * p.kv.page_size, (int64_t)kPxMostRows);
     const int32_t n = p.q_limit ? p.q_limit[u] : p.kv.seq_len[s];
     if (n > room) set_error(CSA2_DEVERR_BAD_ROW);
     return (int32_t)min((int64_t)max(n, 0), room);
@@ -632,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             uint32_t chunk = 0, strips = 0;
             bool ok = true;
             auto scores = [&](int i) {
-                if (i == 0 || wk.tile == 0) ok = ok && mbar_wait(q_full, strips++ & 1u);
+                if (i == 0 || wk.tile == 0) ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(q_full, strips++ & 1u));
 #pragma unroll 1
                 for (int d = 0; d < 4 && ok; ++d, ++chunk) {
                     const uint32_t slot = chunk % kPxSlots;

@@ -75,6 +75,8 @@ def test_prefix_attention_refuses_on_the_host(binding):
     assert call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
     assert call(w=8) == 1 and call(wb=0x6000, w=8) == 1 and call(wb=0x6000, we=0x6100, swa=0x7000, stride=0, w=8) == 1
     assert call(kv=_desc(binding, d=256)) == 2
+    swa = dict(wb=0x6000, we=0x6100, swa=0x7000)
+    assert call(w=1 << 30, stride=8, **swa) == 2 and call(w=8, stride=1 << 30, **swa) == 2
     assert call(wsb=16) == 3 and call(ws=None) == 3 and call(ws=0x10010) == 3
     assert call(n_groups=0, wsb=0) == 0  # nothing to do
     assert binding.csa2_prefix_attn_workspace_size(3, 2, 1, 129) == 0

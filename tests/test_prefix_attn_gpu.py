@@ -265,3 +265,40 @@ def test_out_of_range_q_leaves_other_queries_alone(B, cuda_device):
     B.csa2_device_status()
     for j in (0, 1, 3, 4):
         assert torch.equal(o[int(c.members[j])], keep[int(c.members[j])])
+
+
+def test_a_descending_group_list_computes_nothing(B, cuda_device):
+    c = Case(cuda_device, [2, 2], [100, 64], [5, 80], 16, 64, seed=18)
+    o, _ = c.run(B)
+    B.csa2_device_status()
+    args = list(c.args)
+    for begin in ([0, 4, 2], [2, 0, 4]):
+        args[4] = torch.tensor(begin, dtype=torch.int32, device=cuda_device)
+        o.fill_(77.0)
+        B.csa2_prefix_attn_decode(*args)
+        assert B.csa2_device_status() == 1
+        assert (o == 77.0).all()
+
+
+def test_limits_beyond_the_table_are_cut_and_reported(B, cuda_device):
+    """Two queries ask for more entries than a row of the table holds; the last pages of the rows are not there either."""
+    c = Case(cuda_device, [3], [130], [10, 62, 0], 16, 64, seed=19)
+    c.limit = c.seq_len.copy()
+    c.limit[c.members[0]] = 2 ** 31 - 1
+    c.limit[c.members[2]] = 10 ** 6
+    o, lse = c.run(B)
+    assert B.csa2_device_status() == 1
+    c.limit = np.minimum(c.limit, c.table.shape[1] * c.ps)
+    full = (c.table >= 0).sum(1) * c.ps  # rows of the pages that are there
+    c.limit = np.minimum(c.limit, full).astype(np.int32)
+    c.check(o, lse)
+
+
+def test_empty_groups_and_an_unlisted_batch(B, cuda_device):
+    """Groups without members between others, and a call without groups."""
+    c = Case(cuda_device, [2, 0, 3, 0], [70, 5, 300, 9], [5, 80], 16, 64, seed=20, spare=4)
+    _run(B, c)
+    o = torch.full_like(c.args[13], 77.0)
+    none = torch.empty(0, dtype=torch.int32, device=cuda_device)
+    B.csa2_prefix_attn_decode(*c.args[:3], none, torch.zeros(1, dtype=torch.int32, device=cuda_device), none, *c.args[6:13], o, *c.args[14:])
+    assert (o == 77.0).all() and B.csa2_device_status() == 0
