@@ -1453,7 +1453,7 @@ unsigned copy_blocks(int64_t rows) {
 constexpr int64_t kPxMaxQueries = 1 << 17;
 struct PrefixLayout {
     int32_t pairs, max_pre;
-    size_t off_start, off_start_tile, off_mgroup, off_gstrip, off_gtiles, off_strips, off_q16, off_pre_o, off_pre_lse, off_own_o, off_own_lse, total;
+    size_t off_start, off_start_tile, off_items, off_gseen, off_gstrip, off_gtiles, off_gcost, off_strips, off_q16, off_pre_o, off_pre_lse, off_own_o, off_own_lse, total;
 };
 PrefixLayout prefix_layout(int32_t n_members, int32_t n_groups, int32_t q_per_seq, int32_t h) {
     PrefixLayout L{};
@@ -1468,9 +1468,11 @@ PrefixLayout prefix_layout(int32_t n_members, int32_t n_groups, int32_t q_per_se
     };
     L.off_start = take((size_t)L.pairs * 4);
     L.off_start_tile = take((size_t)(L.pairs + 1) * 8);
-    L.off_mgroup = take((size_t)n_members * 4);
+    L.off_items = take((size_t)n_own * sizeof(PrefixItem));
+    L.off_gseen = take((size_t)n_groups * 4);
     L.off_gstrip = take((size_t)n_groups * 4);
-    L.off_gtiles = take((size_t)n_groups * 8);
+    L.off_gtiles = take((size_t)n_groups * 4);
+    L.off_gcost = take((size_t)n_groups * 8);
     L.off_strips = take((size_t)(L.max_pre + n_own) * sizeof(PrefixStrip));
     L.off_q16 = take((size_t)n_own * h * CSA2_D * 2);
     L.off_pre_o = take((size_t)(L.pairs + L.max_pre) * kPxRows * CSA2_D * 4);
@@ -1693,9 +1695,11 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     p.n_pre = reinterpret_cast<int32_t *>(b + 16);
     p.start = reinterpret_cast<int32_t *>(b + L.off_start);
     p.start_tile = reinterpret_cast<int64_t *>(b + L.off_start_tile);
-    p.member_group = reinterpret_cast<int32_t *>(b + L.off_mgroup);
+    p.items = reinterpret_cast<PrefixItem *>(b + L.off_items);
+    p.group_seen = reinterpret_cast<int32_t *>(b + L.off_gseen);
     p.group_strip = reinterpret_cast<int32_t *>(b + L.off_gstrip);
-    p.group_tiles = reinterpret_cast<int64_t *>(b + L.off_gtiles);
+    p.group_tiles = reinterpret_cast<int32_t *>(b + L.off_gtiles);
+    p.group_cost = reinterpret_cast<int64_t *>(b + L.off_gcost);
     p.strips = reinterpret_cast<PrefixStrip *>(b + L.off_strips);
     p.max_pre = L.max_pre;
     p.q16 = reinterpret_cast<uint16_t *>(b + L.off_q16);

@@ -58,6 +58,16 @@ struct __align__(16) PrefixStrip {
     int32_t w_seq;     // sequence of the window
 };
 
+// What the merge has to know of one query: where the partials of its rows are.
+struct __align__(16) PrefixItem {
+    int64_t pre_cost0, own_cost0;  // cost0 of its group's first strip, of its own strip
+    int32_t pre_strip, pre_tiles;  // first strip of the group, tiles of each (0: none)
+    int32_t x0;                    // its first row among the group's rows
+    int32_t own_tiles;
+    int32_t u;                     // its number, -1: not computed
+    int32_t group;
+};
+
 struct PrefixParams {
     const uint16_t *q;  // bf16 [nq][h][512]
     csa2_kv_desc kv;
@@ -76,9 +86,11 @@ struct PrefixParams {
     int32_t *n_pre;         // [1] prefix strips
     int32_t *start;         // [pairs] first strip of each pair's run
     int64_t *start_tile;    // [pairs + 1] first tile of each run
-    int32_t *member_group;  // [n_members], -1: not computed
-    int32_t *group_strip;   // [n_groups] first strip of a group
-    int64_t *group_tiles;   // [n_groups] tiles of one strip of a group
+    PrefixItem *items;      // [n_members * q_per_seq]
+    // of each group, when there are more than kPxPlanGroups (else in shared memory):
+    // entries of the prefix that any query sees, first strip, its cost0, tiles
+    int32_t *group_seen, *group_strip, *group_tiles;
+    int64_t *group_cost;
     PrefixStrip *strips;    // [max_pre + n_members * q_per_seq], the prefix strips first
     int32_t max_pre;
     uint16_t *q16;          // [n_members * q_per_seq * h][512] q in f16, in the order of members
@@ -172,9 +184,9 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr int kPxStripCost = 2;
 __device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t tiles) { return (int32_t)min((int64_t)pairs, tiles); }
 __device__ __forceinline__ int64_t px_lo(int64_t cost, int32_t pairs, int64_t c) { return c * cost / pairs; }
-// the pair whose share holds tile x of strip t
-__device__ __forceinline__ int32_t px_owner(int64_t cost, int32_t pairs, const PrefixStrip &t, int32_t x) {
-    return (int32_t)(((t.cost0 + kPxStripCost + x + 1) * pairs - 1) / cost);
+// the pair whose share holds tile x of the strip that begins at cost0
+__device__ __forceinline__ int32_t px_owner(int64_t cost, int32_t pairs, int64_t cost0, int32_t x) {
+    return (int32_t)(((cost0 + kPxStripCost + x + 1) * pairs - 1) / cost);
 }
 
 // Visible entries of query u of sequence s: at most what a row of the page table
@@ -188,34 +200,54 @@ __device__ __forceinline__ int32_t px_limit(const PrefixParams &p, int32_t s, in
 }
 
 // ---------------------------------------------------------------------------
-// plan: one block lists the strips
+// plan: one block lists the strips. Its time is that of its dependent loads and
+// barriers, so threads keep what they computed (one query and one strip each, up
+// to 1024) and the groups' numbers stay in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kPxPlanThreads = 1024;
+constexpr int kPxPlanGroups = 1024;
 
-__device__ __forceinline__ int64_t px_block_exclusive(int64_t v, int64_t *warp_sums, int64_t &total) {
+// Exclusive sums of two values over the block, and their totals.
+__device__ __forceinline__ void px_block_exclusive(int64_t (&v)[2], int64_t (*sums)[32], int64_t (&total)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t s = v;
+    int64_t s[2] = {v[0], v[1]};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += u;
-    }
-    if (lane == 31) warp_sums[warp] = s;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s[k], o);
+            if (lane >= o) s[k] += u;
+        }
+    if (lane == 31) sums[0][warp] = s[0], sums[1][warp] = s[1];
     __syncthreads();
-    if (warp == 0) {
-        int64_t w = warp_sums[lane];
+    if (warp < 2) {
+        int64_t w = sums[warp][lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
             if (lane >= o) w += u;
         }
-        warp_sums[lane] = w;
+        sums[warp][lane] = w;
     }
     __syncthreads();
-    const int64_t before = (warp ? warp_sums[warp - 1] : 0) + s - v;
-    total = warp_sums[31];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        v[k] = (warp ? sums[k][warp - 1] : 0) + s[k] - v[k];
+        total[k] = sums[k][31];
+    }
     __syncthreads();
-    return before;
+}
+static_assert(kPxPlanThreads == 1024, "px_block_exclusive sums 32 warps");
+
+// The last k in [0, n) with a[k] <= x of an ascending list; -1: none.
+__device__ __forceinline__ int32_t px_last_below(const int32_t *a, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n;  // a[k] <= x for k < lo, > x for k >= hi
+    while (lo < hi) {
+        const int32_t m = (lo + hi) >> 1;
+        if (a[m] <= x) lo = m + 1;
+        else hi = m;
+    }
+    return lo - 1;
 }
 
 // q in f16 (the sign turned for a negative scale), rows in the order of members:
@@ -247,133 +279,158 @@ __device__ __forceinline__ void px_convert_q(const PrefixParams &p, int64_t rows
     if (bad) set_error(CSA2_DEVERR_Q_RANGE);
 }
 
+// Notes the pairs whose share of the cost begins in strip i.
+__device__ __forceinline__ void px_note_starts(const PrefixParams &p, int32_t i, int64_t tile0, int64_t cost0, int32_t ntiles, int64_t cost,
+                                               int32_t pairs) {
+    if (ntiles == 0) return;
+    // pairs c with cost0 <= lo(c) < cost0 + kPxStripCost + ntiles
+    const int64_t end = cost0 + kPxStripCost + ntiles;
+    for (int64_t c = (cost0 * pairs + cost - 1) / cost; c < pairs && px_lo(cost, pairs, c) < end; ++c) {
+        p.start[c] = i;
+        p.start_tile[c] = tile0 + max((int64_t)0, px_lo(cost, pairs, c) - cost0 - kPxStripCost);
+    }
+}
+
 __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) {
-    __shared__ int64_t sums[32];
+    __shared__ int64_t sums[2][32];
     __shared__ int32_t descends;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int32_t begin_s[kPxPlanGroups + 1], seen_s[kPxPlanGroups], strip_s[kPxPlanGroups], tiles_s[kPxPlanGroups];
+    __shared__ int64_t cost_s[kPxPlanGroups];
+    const int tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
-    const int32_t n_own = p.n_members * p.q_per_seq, ps_rows = p.q_per_seq * p.h;
+    const int32_t n_own = p.n_members * p.q_per_seq, per = p.q_per_seq * p.h;
     if (blockIdx.x > 0) {
         px_convert_q(p, (int64_t)n_own * p.h);
         return;
     }
+    const bool few = p.n_groups <= kPxPlanGroups;
+    const int32_t *begin = few ? begin_s : p.group_begin;
+    // volatile: raised by atomics, which a line in L1 would not show
+    volatile int32_t *seen = few ? seen_s : p.group_seen;
+    int32_t *g_strip = few ? strip_s : p.group_strip, *g_tiles = few ? tiles_s : p.group_tiles;
+    int64_t *g_cost = few ? cost_s : p.group_cost;
     if (tid == 0) descends = 0;
     __syncthreads();
-    for (int32_t g = tid; g < p.n_groups; g += kPxPlanThreads)
-        if (p.group_begin[g] > p.group_begin[g + 1]) descends = 1;
-    for (int32_t j = tid; j < p.n_members; j += kPxPlanThreads) p.member_group[j] = -1;
+    for (int32_t g = tid; g < p.n_groups; g += kPxPlanThreads) {
+        const int32_t b0 = p.group_begin[g], b1 = p.group_begin[g + 1];
+        if (b0 > b1) descends = 1;
+        if (b0 < 0 || b1 > p.n_members) set_error(CSA2_DEVERR_BAD_ROW);
+        if (few) {
+            begin_s[g] = b0;
+            if (g == p.n_groups - 1) begin_s[g + 1] = b1;
+        }
+        seen[g] = 0;
+    }
     __syncthreads();
     // groups that overlap could not be told apart: a list that descends is refused as a whole
     const bool all_bad = descends != 0;
     if (all_bad && tid == 0) set_error(CSA2_DEVERR_BAD_ROW);
     PrefixStrip *own = p.strips + p.max_pre;
-    for (int32_t i = tid; i < n_own; i += kPxPlanThreads) own[i].ntiles = 0;
-    __syncthreads();
-    // a warp per group: its members' lists, and how much of the prefix they see
-    for (int32_t g = warp; g < p.n_groups; g += kPxPlanThreads / 32) {
-        const int32_t b0 = p.group_begin[g], b1 = p.group_begin[g + 1];
-        const bool bad = all_bad || b0 < 0 || b1 > p.n_members;
-        int32_t seen = 0;
-        const int32_t prefix = max(0, p.prefix_len[g]);
-        const int32_t head = bad || b0 >= b1 ? -1 : p.members[b0];
-        if (!bad) {
-            for (int32_t i = b0 * p.q_per_seq + lane; i < b1 * p.q_per_seq; i += 32) {
-                const int32_t j = i / p.q_per_seq, qi = i - j * p.q_per_seq;
-                const int32_t s = p.members[j];
-                const int64_t u = (int64_t)s * p.q_per_seq + qi;
-                if (s < 0 || s >= p.kv.batch) {
-                    set_error(CSA2_DEVERR_BAD_ROW);
-                    continue;
-                }
-                p.member_group[j] = g;
-                if (u >= p.nq) continue;
-                const int32_t limit = px_limit(p, s, u);
-                seen = max(seen, min(limit, prefix));
-                int32_t wb = 0, nw = 0;
-                if (p.swa_begin) {
-                    wb = p.swa_begin[u];
-                    nw = max(0, p.swa_end[u] - wb);
-                    if (nw > 0 && (wb < 0 || wb >= p.swa_seq_stride || nw > p.swa_seq_stride || nw > p.w_max)) {
-                        set_error(CSA2_DEVERR_BAD_ROW);
-                        nw = 0;
-                    }
-                }
-                PrefixStrip t;
-                t.tile0 = t.cost0 = 0;
-                t.entries = max(0, limit - prefix);
-                t.rows = t.entries + nw;
-                t.ntiles = (int32_t)(((int64_t)t.rows + kPxTile - 1) / kPxTile);
-                t.seq = s;
-                t.t_base = prefix;
-                t.w_begin = wb;
-                t.q_rows = p.h;
-                t.member0 = -1;
-                t.row0 = 0;
-                t.q_at = i * p.h;
-                t.w_seq = s;
-                own[i] = t;
+    // ---- each query's own list, and how much of the prefix it sees ----
+    int32_t my_tiles = 0;        // of the thread's first query
+    PrefixItem my_item;
+    my_item.u = -1;
+    for (int32_t i = tid; i < n_own; i += kPxPlanThreads) {
+        const int32_t j = i / p.q_per_seq, qi = i - j * p.q_per_seq;
+        const int32_t s = p.members[j];
+        const int64_t u = (int64_t)s * p.q_per_seq + qi;
+        const bool there = s >= 0 && s < p.kv.batch;
+        if (!there) set_error(CSA2_DEVERR_BAD_ROW);
+        int32_t limit = 0, wb = 0, nw = 0;
+        if (there && u < p.nq) {
+            limit = px_limit(p, s, u);
+            if (p.swa_begin) {
+                wb = p.swa_begin[u];
+                nw = max(0, p.swa_end[u] - wb);
             }
-        } else if (lane == 0) {
-            set_error(CSA2_DEVERR_BAD_ROW);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) seen = max(seen, __shfl_xor_sync(0xFFFFFFFFu, seen, o));
-        if (lane == 0) p.group_tiles[g] = head < 0 || head >= p.kv.batch ? 0 : ((int64_t)seen << 32) | (uint32_t)((seen + kPxTile - 1) / kPxTile);
+        const int32_t g = all_bad ? -1 : px_last_below(begin, p.n_groups + 1, j);
+        PrefixItem item;
+        item.u = -1;
+        item.group = -1;
+        item.own_tiles = 0;
+        if (there && u < p.nq && g >= 0 && g < p.n_groups && begin[g] >= 0 && begin[g + 1] <= p.n_members) {
+            const int32_t prefix = max(0, p.prefix_len[g]), b0 = begin[g], head = p.members[b0];
+            if (head >= 0 && head < p.kv.batch && min(limit, prefix) > 0) atomicMax(const_cast<int32_t *>(seen) + g, min(limit, prefix));
+            if (nw > 0 && (wb < 0 || wb >= p.swa_seq_stride || nw > p.swa_seq_stride || nw > p.w_max)) {
+                set_error(CSA2_DEVERR_BAD_ROW);
+                nw = 0;
+            }
+            PrefixStrip t;
+            t.tile0 = t.cost0 = 0;
+            t.entries = max(0, limit - prefix);
+            t.rows = t.entries + nw;
+            t.ntiles = (t.rows + kPxTile - 1) / kPxTile;
+            t.seq = s;
+            t.t_base = prefix;
+            t.w_begin = wb;
+            t.q_rows = p.h;
+            t.member0 = -1;
+            t.row0 = 0;
+            t.q_at = i * p.h;
+            t.w_seq = s;
+            own[i] = t;
+            item.u = (int32_t)u;
+            item.group = g;
+            item.x0 = (j - b0) * per + qi * p.h;
+            item.own_tiles = t.ntiles;
+        } else {
+            own[i].ntiles = 0;
+        }
+        if (i == tid) {
+            my_tiles = item.own_tiles;
+            my_item = item;
+        } else {
+            p.items[i] = item;
+        }
     }
     __syncthreads();
-    // prefix strips: where each group's start, and their tiles
-    int64_t strips = 0, tiles = 0, cost = 0;
+    // ---- the groups' strips ----
+    int64_t strips = 0, tiles = 0;
     for (int32_t g0 = 0; g0 < p.n_groups; g0 += kPxPlanThreads) {
         const int32_t g = g0 + tid;
-        int32_t n = 0, nt = 0, seen = 0, b0 = 0, rows = 0;
-        if (g < p.n_groups && p.group_tiles[g] != 0) {
-            b0 = p.group_begin[g];
-            rows = (p.group_begin[g + 1] - b0) * ps_rows;
-            n = (rows + kPxRows - 1) / kPxRows;
-            nt = (int32_t)(p.group_tiles[g] & 0xFFFFFFFF);
-            seen = (int32_t)(p.group_tiles[g] >> 32);
+        int32_t n = 0, nt = 0;
+        if (g < p.n_groups && seen[g] > 0) {
+            n = ((begin[g + 1] - begin[g]) * per + kPxRows - 1) / kPxRows;
+            nt = (seen[g] + kPxTile - 1) / kPxTile;
         }
-        int64_t ts, tt;
-        const int64_t s0 = strips + px_block_exclusive(n, sums, ts);
-        const int64_t t0 = tiles + px_block_exclusive((int64_t)n * nt, sums, tt);
-        const int64_t c0 = t0 + kPxStripCost * s0;  // every prefix strip has tiles
-        if (g < p.n_groups) p.group_strip[g] = n ? (int32_t)s0 : -1;
-        for (int32_t x = 0; x < n && s0 + x < p.max_pre; ++x) {
-            PrefixStrip t;
-            t.tile0 = t0 + (int64_t)x * nt;
-            t.cost0 = c0 + (int64_t)x * (nt + kPxStripCost);
-            t.ntiles = nt;
-            t.rows = seen;
-            t.seq = p.members[b0];
-            t.t_base = 0;
-            t.entries = seen;
-            t.w_begin = 0;
-            t.q_rows = min(kPxRows, rows - x * kPxRows);
-            t.member0 = b0;
-            t.row0 = x * kPxRows;
-            t.q_at = b0 * ps_rows + x * kPxRows;
-            t.w_seq = 0;
-            p.strips[s0 + x] = t;
+        int64_t v[2] = {n, (int64_t)n * nt}, t[2];
+        px_block_exclusive(v, sums, t);
+        if (g < p.n_groups) {
+            g_strip[g] = (int32_t)(strips + v[0]);
+            g_tiles[g] = nt;
+            g_cost[g] = tiles + v[1] + kPxStripCost * (strips + v[0]);  // every prefix strip has tiles
         }
-        strips += ts;
-        tiles += tt;
+        strips += t[0];
+        tiles += t[1];
     }
-    const int32_t n_pre = (int32_t)strips;
-    cost = tiles + kPxStripCost * strips;
+    const int32_t n_pre = (int32_t)min(strips, (int64_t)p.max_pre);
+    __syncthreads();
+    int64_t cost = tiles + kPxStripCost * strips;
+    // ---- where each query's own strip lies ----
+    int64_t my_tile0 = 0, my_cost0 = 0;
     for (int32_t i0 = 0; i0 < n_own; i0 += kPxPlanThreads) {
         const int32_t i = i0 + tid;
-        int64_t tt;
-        const int32_t nt = i < n_own ? own[i].ntiles : 0;
-        const int64_t t0 = tiles + px_block_exclusive(nt, sums, tt);
-        int64_t cc;
-        const int64_t c0 = cost + px_block_exclusive(nt ? nt + kPxStripCost : 0, sums, cc);
+        PrefixItem item = my_item;
+        if (i0 > 0 && i < n_own) item = p.items[i];
+        const int32_t nt = i < n_own ? item.own_tiles : 0;
+        int64_t v[2] = {nt, nt ? nt + kPxStripCost : 0}, t[2];
+        px_block_exclusive(v, sums, t);
         if (i < n_own) {
-            own[i].tile0 = t0;
-            own[i].cost0 = c0;
+            own[i].tile0 = tiles + v[0];
+            own[i].cost0 = cost + v[1];
+            item.own_cost0 = cost + v[1];
+            if (item.group >= 0) {
+                item.pre_strip = g_strip[item.group];
+                item.pre_tiles = g_tiles[item.group];
+                item.pre_cost0 = g_cost[item.group];
+            }
+            p.items[i] = item;
+            if (i0 == 0) my_tile0 = tiles + v[0], my_cost0 = cost + v[1];
         }
-        tiles += tt;
-        cost += cc;
+        tiles += t[0];
+        cost += t[1];
     }
     const int32_t pairs = px_pairs(p.pairs, tiles);
     if (tid == 0) {
@@ -383,16 +440,29 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
         p.start_tile[pairs] = tiles;
     }
     if (tiles == 0) return;
-    // where each pair's share begins: its first strip and tile
-    for (int32_t i = tid; i < n_pre + n_own; i += kPxPlanThreads) {
-        const PrefixStrip &t = i < n_pre ? p.strips[i] : own[i - n_pre];
-        if (t.ntiles == 0) continue;
-        // pairs c with cost0 <= lo(c) < cost0 + kPxStripCost + ntiles
-        const int64_t end = t.cost0 + kPxStripCost + t.ntiles;
-        for (int64_t c = (t.cost0 * pairs + cost - 1) / cost; c < pairs && px_lo(cost, pairs, c) < end; ++c) {
-            p.start[c] = i;
-            p.start_tile[c] = t.tile0 + max((int64_t)0, px_lo(cost, pairs, c) - t.cost0 - kPxStripCost);
-        }
+    // ---- the prefix strips, and where each pair's share begins ----
+    for (int32_t s = tid; s < n_pre; s += kPxPlanThreads) {
+        const int32_t g = px_last_below(g_strip, p.n_groups, s);  // of equal ones the last: the group that has strips
+        const int32_t x = s - g_strip[g], b0 = begin[g], rows = (begin[g + 1] - b0) * per;
+        PrefixStrip t;
+        t.ntiles = g_tiles[g];
+        t.cost0 = g_cost[g] + (int64_t)x * (t.ntiles + kPxStripCost);
+        t.tile0 = t.cost0 - (int64_t)kPxStripCost * s;
+        t.rows = t.entries = seen[g];
+        t.seq = p.members[b0];
+        t.t_base = 0;
+        t.w_begin = 0;
+        t.q_rows = min(kPxRows, rows - x * kPxRows);
+        t.member0 = b0;
+        t.row0 = x * kPxRows;
+        t.q_at = b0 * per + x * kPxRows;
+        t.w_seq = 0;
+        p.strips[s] = t;
+        px_note_starts(p, s, t.tile0, t.cost0, t.ntiles, cost, pairs);
+    }
+    for (int32_t i = tid; i < n_own; i += kPxPlanThreads) {
+        if (i == tid) px_note_starts(p, n_pre + i, my_tile0, my_cost0, my_tiles, cost, pairs);
+        else px_note_starts(p, n_pre + i, own[i].tile0, own[i].cost0, own[i].ntiles, cost, pairs);
     }
 }
 
@@ -1090,28 +1160,23 @@ __global__ void __launch_bounds__(kPxMergeThreads) k_prefix_merge(PrefixParams p
     pdl_wait();
     const int tid = threadIdx.x;
     const int32_t i = blockIdx.x, head = blockIdx.y;
-    const int32_t j = i / p.q_per_seq, qi = i - j * p.q_per_seq;
-    const int32_t g = p.member_group[j];
-    if (g < 0) return;
-    const int64_t u = (int64_t)p.members[j] * p.q_per_seq + qi;
-    if (u >= p.nq) return;
+    const PrefixItem item = p.items[i];
     const int64_t cost = p.total_tiles[1];
     const int32_t pairs = px_pairs(p.pairs, p.total_tiles[0]);
+    if (item.u < 0) return;
+    const int64_t u = item.u;
     int32_t na = 0, nb = 0;
     int64_t a0 = 0, b0 = 0;  // first rows of the partials
-    const int32_t s0 = p.group_strip[g];
-    if (s0 >= 0) {
-        const int32_t x = ((j - p.group_begin[g]) * p.q_per_seq + qi) * p.h + head;
-        const int32_t s = s0 + x / kPxRows;
-        const PrefixStrip t = p.strips[s];
-        const int32_t c = px_owner(cost, pairs, t, 0);
-        na = px_owner(cost, pairs, t, t.ntiles - 1) - c + 1;
-        a0 = ((int64_t)c + s) * kPxRows + x % kPxRows;
+    if (item.pre_tiles > 0) {
+        const int32_t x = item.x0 + head, s = x / kPxRows;
+        const int64_t c0 = item.pre_cost0 + (int64_t)s * (item.pre_tiles + kPxStripCost);
+        const int32_t c = px_owner(cost, pairs, c0, 0);
+        na = px_owner(cost, pairs, c0, item.pre_tiles - 1) - c + 1;
+        a0 = ((int64_t)c + item.pre_strip + s) * kPxRows + x % kPxRows;
     }
-    const PrefixStrip t = p.strips[p.max_pre + i];
-    if (t.ntiles > 0) {
-        const int32_t c = px_owner(cost, pairs, t, 0);
-        nb = px_owner(cost, pairs, t, t.ntiles - 1) - c + 1;
+    if (item.own_tiles > 0) {
+        const int32_t c = px_owner(cost, pairs, item.own_cost0, 0);
+        nb = px_owner(cost, pairs, item.own_cost0, item.own_tiles - 1) - c + 1;
         b0 = ((int64_t)c + i) * p.h + head;
     }
     const int32_t np = na + nb;
