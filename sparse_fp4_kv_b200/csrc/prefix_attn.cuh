@@ -178,11 +178,11 @@ __device__ __forceinline__ float ex2(float x) {
 // ---------------------------------------------------------------------------
 // the split of the tile list over the pairs: equal shares of a cost of one per
 // tile and kPxStripCost per strip (loading its q, filling the pipeline and
-// storing its partial). No more pairs than tiles, so that a strip's partials are
-// those of consecutive pairs.
+// storing its partial). No more pairs than the cost, so that a strip's partials
+// are those of consecutive pairs.
 // ---------------------------------------------------------------------------
 constexpr int kPxStripCost = 2;
-__device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t tiles) { return (int32_t)min((int64_t)pairs, tiles); }
+__device__ __forceinline__ int32_t px_pairs(int32_t pairs, int64_t cost) { return (int32_t)min((int64_t)pairs, cost); }
 __device__ __forceinline__ int64_t px_lo(int64_t cost, int32_t pairs, int64_t c) { return c * cost / pairs; }
 // the pair whose share holds tile x of the strip that begins at cost0
 __device__ __forceinline__ int32_t px_owner(int64_t cost, int32_t pairs, int64_t cost0, int32_t x) {
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kPxPlanThreads) k_prefix_plan(PrefixParams p) 
         tiles += t[0];
         cost += t[1];
     }
-    const int32_t pairs = px_pairs(p.pairs, tiles);
+    const int32_t pairs = px_pairs(p.pairs, cost);
     if (tid == 0) {
         p.total_tiles[0] = tiles;
         p.total_tiles[1] = cost;
@@ -677,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
     pdl_wait();
 
     const int32_t c = blockIdx.x >> 1;
-    const int32_t pairs = px_pairs(p.pairs, *p.total_tiles);
+    const int32_t pairs = px_pairs(p.pairs, p.total_tiles[1]);
     const int64_t x0 = c < pairs ? p.start_tile[c] : 0;
     const int n = c < pairs ? (int)(p.start_tile[c + 1] - x0) : 0;
     constexpr uint32_t kColS = 256;
@@ -1119,10 +1119,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int row = 2 * j + (lane >> 4);
-                        const float4 o = *reinterpret_cast<const float4 *>(stage + row * 256 + (((lane ^ row) & 15) << 4));
-                        if (whose >> row & 1u) *(reinterpret_cast<float4 *>(dst + (int64_t)row * CSA2_D + k) + (lane & 15)) = o;
+                    for (int j0 = 0; j0 < 16; j0 += 8) {
+                        float4 o[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = 2 * (j0 + j) + (lane >> 4);
+                            o[j] = *reinterpret_cast<const float4 *>(stage + row * 256 + (((lane ^ row) & 15) << 4));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = 2 * (j0 + j) + (lane >> 4);
+                            if (whose >> row & 1u) __stcg(reinterpret_cast<float4 *>(dst + (int64_t)row * CSA2_D + k) + (lane & 15), o[j]);
+                        }
                     }
                     __syncwarp();
                 }
@@ -1162,7 +1170,7 @@ __global__ void __launch_bounds__(kPxMergeThreads) k_prefix_merge(PrefixParams p
     const int32_t i = blockIdx.x, head = blockIdx.y;
     const PrefixItem item = p.items[i];
     const int64_t cost = p.total_tiles[1];
-    const int32_t pairs = px_pairs(p.pairs, p.total_tiles[0]);
+    const int32_t pairs = px_pairs(p.pairs, cost);
     if (item.u < 0) return;
     const int64_t u = item.u;
     int32_t na = 0, nb = 0;
