@@ -1001,7 +1001,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             const uint4 vw = *reinterpret_cast<const uint4 *>(infos[i % kPxInfos].valid + half * 4);
             __syncwarp();
             if (lane == 0) mbar_arrive(&info_empty[i % kPxInfos]);
-            if (__any_sync(0xFFFFFFFFu, lim < 128 || (vw.x & vw.y & vw.z & vw.w) != 0xFFFFFFFFu)) {
+            // (rows that are none need no masks: what becomes of them reaches no other row)
+            if (__any_sync(0xFFFFFFFFu, sees >= 0 && (lim < 128 || (vw.x & vw.y & vw.z & vw.w) != 0xFFFFFFFFu))) {
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     const int m = lim - 32 * k;
