@@ -251,8 +251,9 @@ __device__ __forceinline__ int32_t px_last_below(const int32_t *a, int32_t n, in
 }
 
 // q in f16 (the sign turned for a negative scale), rows in the order of members:
-// the rows of a strip then lie together and one tiled copy a block of 64 values
-// brings them into shared memory, swizzled. 16 bytes a thread.
+// the rows of a strip then lie together and one tiled copy a block of 64
+// positions brings them into shared memory, swizzled. The latent values stand in
+// the order that the cache's rows get (PxRaw). 16 bytes a thread.
 __device__ __forceinline__ void px_convert_q(const PrefixParams &p, int64_t rows) {
     const int64_t step = (int64_t)(gridDim.x - 1) * kPxPlanThreads;
     bool bad = false;
@@ -260,12 +261,16 @@ __device__ __forceinline__ void px_convert_q(const PrefixParams &p, int64_t rows
         const int32_t row = (int32_t)(i / (CSA2_D / 8)), c = (int32_t)(i % (CSA2_D / 8));
         const int32_t per = p.q_per_seq * p.h, j = row / per, y = row - j * per;
         const int32_t seq = p.members[j];
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
         if (seq >= 0 && seq < p.kv.batch) {
             const int64_t u = (int64_t)seq * p.q_per_seq + y / p.h;
-            if (u < p.nq) v = __ldg(reinterpret_cast<const uint4 *>(p.q + (u * p.h + y % p.h) * CSA2_D) + c);
+            if (u < p.nq) {
+                // piece m of a 128: pairs 32 q + 2 m
+                const uint32_t *at = reinterpret_cast<const uint32_t *>(p.q + (u * p.h + y % p.h) * CSA2_D) + (c >> 4) * 64 + (c & 15);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = __ldg(at + 16 * k);
+            }
         }
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -539,15 +544,19 @@ struct __align__(16) PxInfo {
     int32_t seq, t_base, entries, rows, w_begin, w_seq;  // as in the strip
 };
 
-// A lane's share of a chunk: four units of 32 values (16 bytes of codes and 2
-// of scales, or 32 bytes of a window row), of rows that are 8 (keys) or 4
-// (values) apart. What bounds the kernel is the shared-memory and L1 array: the
-// products' operands (some 3070 cycles a tile), the stores of dequantised rows
-// (2300), and every line that a quarter warp's load touches. So a quarter warp
-// takes whole 64-byte runs of two rows (keys) or 128 bytes of one (values); with
-// four rows of 32 bytes the loads took 3700 cycles of the tile's 9660. The loads
-// are predicated instructions on registers that nothing else merges into, so
-// none waits for another.
+// A lane's share of a chunk: four units of 32 consecutive values of a row (16
+// bytes of codes and 2 of scales, or 32 bytes of a window row). A warp's unit is
+// eight rows of 128 values, four lanes a row, so that its loads take whole
+// 64-byte runs (lanes with a row each touched 32 lines a load, which made the L1
+// array the bound), and its stores are 8 x 8 matrices: lane 4 r + q holds the
+// pair of values that stmatrix puts at columns 2 q, 2 q + 1 of row r. To need no
+// exchange between lanes, the latent values of each 128 are taken in the order
+//     position 8 m + 2 q + e  <-  value 32 q + 2 m + e   (m < 16, q < 4, e < 2),
+// pair m of lane q's unit being what it stores to matrix m. The products do not
+// mind an order of the latent axis: q is converted in the same one, and the
+// columns of O are put back when a partial is stored. The loads are predicated
+// instructions on registers that nothing else merges into, so none waits for
+// another.
 struct PxRaw {
     uint32_t v[4][4], sc[4];
 };
@@ -560,54 +569,59 @@ __device__ __forceinline__ void px_ld16(uint32_t *v, const void *at, bool take) 
 __device__ __forceinline__ void px_ld4(uint32_t &v, const void *at, bool take) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)take));
 }
-// Two units of a run, their rows STEP apart.
-template <int STEP>
+// Units u0 and u0 + 1 of a run: `row` the lane's, the second unit ROWS rows and
+// VALUES values further on.
+template <int ROWS, int VALUES>
 __device__ __forceinline__ void px_fetch_run(const PrefixParams &p, int64_t row, int d0, PxRaw &raw, int u0) {
     const uint8_t *at = p.kv.codes + row * (CSA2_D / 2) + d0 / 2;
+    // the aligned word that holds the unit's two scales
     const uint8_t *sc = p.kv.scales + row * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        px_ld16(raw.v[u0 + u], at + u * STEP * (CSA2_D / 2), true);
-        px_ld4(raw.sc[u0 + u], sc + u * STEP * (CSA2_D / CSA2_BLOCK), true);
+        px_ld16(raw.v[u0 + u], at + u * (ROWS * (CSA2_D / 2) + VALUES / 2), true);
+        px_ld4(raw.sc[u0 + u], sc + u * (ROWS * (CSA2_D / CSA2_BLOCK) + VALUES / CSA2_BLOCK), true);
     }
 }
-__device__ __forceinline__ void px_swap(uint32_t &a, uint32_t &b, bool yes) {
-    const uint32_t x = yes ? b : a, y = yes ? a : b;
-    a = x;
-    b = y;
+// Four matrices of 8 rows by 16 bytes; lane l gives the address of row l % 8 of
+// matrix l / 8.
+__device__ __forceinline__ void px_stm(uint32_t addr, const uint32_t (&h)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                 : "memory");
 }
-// A unit of FP4 values dequantised into four 16-byte pieces of a swizzled
-// 128-byte row: piece j at dst + (o0 ^ 16 j). The units that a quarter warp
-// stores lie in several blocks; each lane starts with another piece (turn, by
-// block), so that its eight stores meet eight different bank groups. sc: the
-// unit's two scales.
-__device__ __forceinline__ void px_store_fp4(const uint32_t (&raw)[4], uint32_t sc, uint8_t *dst, uint32_t o0, int turn) {
-    uint32_t w[4] = {raw[0], raw[1], raw[2], raw[3]};
+// Matrices 4 j .. 4 j + 3 of a unit: a block of 64 positions is a 128-byte row,
+// swizzled by its number, so matrices 4 to 7 lie 64 bytes across from 0 to 3
+// (addr's own swizzle included) and 8 to 15 in the next block.
+__device__ __forceinline__ uint32_t px_matrix(uint32_t addr, int j, uint32_t block) { return (j & 1 ? addr ^ 64u : addr) + (j >> 1) * block; }
+// Words of FP4 codes and the unit's two scales -> f16 pairs -> matrices.
+__device__ __forceinline__ void px_store_fp4(const uint32_t (&w)[4], uint32_t sc, uint32_t addr, uint32_t block) {
     const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)sc);
-    uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
-    px_swap(w[0], w[1], turn & 1);
-    px_swap(w[2], w[3], turn & 1);
-    px_swap(w[0], w[2], turn & 2);
-    px_swap(w[1], w[3], turn & 2);
-    px_swap(f[0], f[1], turn & 2);
-    const uint32_t o = o0 ^ ((uint32_t)turn << 4);
+    const uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t h[4];
         e2m1x8_to_f16x8(w[j], h);
-        *reinterpret_cast<uint4 *>(dst + (o ^ (j << 4))) = make_uint4(hmul2_u32(h[0], f[j >> 1]), hmul2_u32(h[1], f[j >> 1]),
-                                                                     hmul2_u32(h[2], f[j >> 1]), hmul2_u32(h[3], f[j >> 1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = hmul2_u32(h[k], f[j >> 1]);
+        px_stm(px_matrix(addr, j, block), h);
     }
 }
-// A unit of a window row (raw: its first 16 bytes).
-__device__ __forceinline__ void px_store_e4m3(const uint32_t (&raw)[4], const uint4 &m, uint8_t *dst, uint32_t o0) {
+// Pairs of a window row's unit: its first 16 bytes (raw) and its last (m).
+__device__ __forceinline__ void px_pairs_e4m3(const uint32_t (&raw)[4], const uint4 &m, uint32_t (&h)[16]) {
     const uint32_t w[8] = {raw[0], raw[1], raw[2], raw[3], m.x, m.y, m.z, m.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4 *>(dst + (o0 ^ (j << 4))) = make_uint4(
-            e4m3x2_to_f16x2((uint16_t)(w[2 * j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j] >> 16)),
-            e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w[2 * j + 1] >> 16)));
+    for (int j = 0; j < 8; ++j) {
+        h[2 * j] = e4m3x2_to_f16x2((uint16_t)(w[j] & 0xFFFFu));
+        h[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(w[j] >> 16));
+    }
 }
+__device__ __forceinline__ void px_store_pairs(const uint32_t (&h)[16], uint32_t addr, uint32_t block) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x[4] = {h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]};
+        px_stm(px_matrix(addr, j, block), x);
+    }
+}
+
 // Entries that row r of a strip sees of the strip's list; -1 where there is no
 // such row.
 __device__ __forceinline__ int32_t px_sees(const PrefixParams &p, const PrefixStrip &t, int r) {
@@ -834,12 +848,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         // ---- rows of the cache into the ring: four sets of four warps, a slot of
         // the ring each, so that a set never waits for a phase that another has
         // yet to begin. Chunk x of the call goes to slot x % 4. Lane l of a warp has
-        //   keys: rows 8 u + l / 4 of the warp's 32, unit l % 4 of the chunk's 128
-        //     values;
-        //   values: rows 4 u + l / 8 of its 16, unit l % 8 of 256 ----
+        //   keys: rows 8 u + l / 4 of the warp's 32, values 32 (l % 4) .. of the chunk's
+        //     128;
+        //   values: rows 8 (u / 2) + l / 4 of its 16, values 128 (u % 2) + 32 (l % 4) ..
+        //     of the CTA's 256 ----
         const int set = (warp - kPxSoftWarps) >> 2, lw = (warp - kPxSoftWarps) & 3;
         const uint32_t full_addr = cluster_smem_addr(&full[set], 0);
-        const int k_sub = lane >> 2, v_sub = lane >> 3;
+        const int sub = lane >> 2;
+        // row lane % 8 of matrix lane / 8, in the slot, swizzled
+        const uint32_t stm_addr = smem_u32(ring) + set * kPxSlotBytes + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
         PxRaw raw;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -854,14 +871,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
         bool keys = true, skip = false;
         int d = set;  // which of the group's chunks is the set's
         auto value0 = [&]() {
-            return keys ? 128 * d + 32 * (lane & 3) : 256 * (int)rank + 32 * (lane & 7);
+            return (keys ? 128 * d : 256 * (int)rank) + 32 * (lane & 3);
         };
         // The window ring of a tile; of a run of window rows, the lane's first unit.
         auto ring_of = [&](const PxInfo &f) { return p.swa + (int64_t)f.w_seq * p.swa_seq_stride * CSA2_D; };
         auto run_of = [&](const PxInfo &f) {
             const int32_t b0 = f.base[keys ? 8 * (int)rank + 2 * lw : 4 * d + lw];
-            return ring_of(f) + (int64_t)(kPxWindow - b0 + (keys ? k_sub : v_sub)) * CSA2_D + value0();
+            return ring_of(f) + (int64_t)(kPxWindow - b0 + sub) * CSA2_D + value0();
         };
+        auto window_step = [&](int u) { return keys ? u * 8 * CSA2_D : (u >> 1) * 8 * CSA2_D + (u & 1) * 128; };
         // Fetches the set's chunk of tile i's keys or values, a group whose first
         // chunk is number `first`.
         auto fetch = [&](int i, bool of_keys, uint32_t first) {
@@ -874,16 +892,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             const int d0 = value0();
             if (kind == kRunEntries) {
                 if (keys) {
-                    px_fetch_run<8>(p, (int64_t)b0 + k_sub, d0, raw, 0);
-                    px_fetch_run<8>(p, (int64_t)b1 + k_sub, d0, raw, 2);
+                    px_fetch_run<8, 0>(p, (int64_t)b0 + sub, d0, raw, 0);
+                    px_fetch_run<8, 0>(p, (int64_t)b1 + sub, d0, raw, 2);
                 } else {
-                    px_fetch_run<4>(p, (int64_t)b0 + v_sub, d0, raw, 0);
-                    px_fetch_run<4>(p, (int64_t)b0 + 8 + v_sub, d0, raw, 2);
+                    px_fetch_run<0, 128>(p, (int64_t)b0 + sub, d0, raw, 0);
+                    px_fetch_run<0, 128>(p, (int64_t)b0 + 8 + sub, d0, raw, 2);
                 }
             } else if (kind == kRunWindow && !skip) {
                 const uint8_t *at = run_of(f);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], at + u * (keys ? 8 : 4) * CSA2_D, true);
+                for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], at + window_step(u), true);
             }
         };
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[0], 0));
@@ -899,54 +917,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 if (round > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[set], (round - 1) & 1u));
                 if (!ok) break;
                 ++round;
-                // blocks of 64 values: keys [128 rows][128 B], values [64 rows][128 B]
-                uint8_t *s = ring + set * kPxSlotBytes;
-                const int blk = (lane >> 1) & (keys ? 1 : 3), turn = keys ? 2 * blk : blk;
-                s += keys ? blk * 16384 + (32 * lw + k_sub) * 128 : blk * 8192 + (16 * lw + v_sub) * 128;
-                const uint32_t o0 = (uint32_t)((4 * (lane & 1)) ^ (keys ? k_sub : v_sub)) << 4;
-                const uint32_t o1 = keys ? o0 : o0 ^ 64u;  // rows 4 further on swap the halves of the swizzle
-                const int step = keys ? 8 * 128 : 4 * 128;
+                // blocks of 64 positions: keys [128 rows][128 B], values [64 rows][128 B]
+                const uint32_t block = keys ? 16384u : 8192u;
+                const uint32_t at0 = stm_addr + (uint32_t)lw * (keys ? 4096u : 2048u);
+                auto unit = [&](int u) { return at0 + (keys ? u * 1024u : (u >> 1) * 1024u + (u & 1) * 16384u); };
                 if (kind == kRunEntries) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), s + u * step, u & 1 ? o1 : o0, turn);
+                    for (int u = 0; u < 4; ++u) px_store_fp4(raw.v[u], raw.sc[u] >> (16 * (lane & 1)), unit(u), block);
                 } else if (kind == kRunWindow) {
                     // the second halves of the units, of sectors that the first ones brought
                     const uint8_t *at = run_of(infos[tile % kPxInfos]) + 16;
 #pragma unroll
-                    for (int v = 0; v < 4; v += 2) {
-                        uint4 m[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) m[u] = __ldg(reinterpret_cast<const uint4 *>(at + (v + u) * (keys ? 8 : 4) * CSA2_D));
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) px_store_e4m3(raw.v[v + u], m[u], s + (v + u) * step, u & 1 ? o1 : o0);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t h[16];
+                        px_pairs_e4m3(raw.v[u], __ldg(reinterpret_cast<const uint4 *>(at + window_step(u))), h);
+                        px_store_pairs(h, unit(u), block);
                     }
                 } else {  // few chunks: resolved (a row a lane) and loaded only here, which spares registers
                     const PxInfo &f = infos[tile % kPxInfos];
                     PxLook look;
                     px_look(p, f, f.tile, keys ? 128 * (int)rank + 32 * lw + lane : 64 * d + 16 * lw + (lane & 15), look);
                     const int32_t rows = px_row(p, look);
-                    const int d0 = value0();
-#pragma unroll
+#pragma unroll 1
                     for (int u = 0; u < 4; ++u) {
-                        const int32_t src = __shfl_sync(0xFFFFFFFFu, rows, keys ? 8 * u + k_sub : 4 * u + v_sub);
-                        uint8_t *to = s + u * step;
-                        const uint32_t o = u & 1 ? o1 : o0;
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        const int32_t src = __shfl_sync(0xFFFFFFFFu, rows, (keys ? 8 * u : 8 * (u >> 1)) + sub);
+                        const int d0 = value0() + (keys ? 0 : 128 * (u & 1));
+                        uint32_t h[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) h[k] = 0u;
                         if (src >= 0) {
-                            v = __ldg(reinterpret_cast<const uint4 *>(p.kv.codes + (int64_t)src * (CSA2_D / 2) + d0 / 2));
-                            const uint16_t sc = __ldg(reinterpret_cast<const uint16_t *>(p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + d0 / CSA2_BLOCK));
+                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.kv.codes + (int64_t)src * (CSA2_D / 2) + d0 / 2));
+                            const uint32_t s2 = e4m3x2_to_f16x2(
+                                __ldg(reinterpret_cast<const uint16_t *>(p.kv.scales + (int64_t)src * (CSA2_D / CSA2_BLOCK) + d0 / CSA2_BLOCK)));
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            px_store_fp4(w, sc, to, o, turn);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t x[4];
+                                e2m1x8_to_f16x8(w[j], x);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) h[4 * j + k] = hmul2_u32(x[k], __byte_perm(s2, 0, j < 2 ? 0x1010 : 0x3232));
+                            }
                         } else if (src != kPxNone) {
                             const uint8_t *at = ring_of(f) + (int64_t)(-2 - src) * CSA2_D + d0;
-                            v = __ldg(reinterpret_cast<const uint4 *>(at));
+                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at));
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            px_store_e4m3(w, __ldg(reinterpret_cast<const uint4 *>(at + 16)), to, o);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + (o ^ (k << 4))) = v;
+                            px_pairs_e4m3(w, __ldg(reinterpret_cast<const uint4 *>(at + 16)), h);
                         }
+                        __syncwarp();
+                        px_store_pairs(h, unit(u), block);
                     }
                 }
                 fence_proxy_async_smem();
@@ -1098,9 +1116,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (ok) ok = mbar_wait(pv_done, (uint32_t)i & 1u);
                 tc_fence_after();
-                // O / l through the P buffer (free now), 64 columns at a time: a thread
-                // has 256 bytes of its row there, in 16-byte units turned by its lane;
-                // half a warp then stores a row's 256 bytes
+                // O / l through the P buffer (free now), 64 positions at a time (half of a
+                // 128: matrices m0 .. m0 + 7): a thread has 256 bytes of its row there, in
+                // 16-byte units turned by its lane; unit 4 q + t is values 32 q + 2 m0 + 4 t
+                // .. + 3, and half a warp stores a row's units to their places
                 const bool mine = ok && sees >= 0;
                 const uint32_t whose = __ballot_sync(0xFFFFFFFFu, mine);
                 uint8_t *stage = p_s + warp * 8192;
@@ -1114,9 +1133,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4 *>(stage + lane * 256 + (((8 * y + j) ^ (lane & 15)) << 4)) =
-                                make_float4(__uint_as_float(v[4 * j]) * inv, __uint_as_float(v[4 * j + 1]) * inv,
-                                            __uint_as_float(v[4 * j + 2]) * inv, __uint_as_float(v[4 * j + 3]) * inv);
+                        {
+                            // positions 32 y + 8 m + 2 q + e: this half's matrices 4 y + m
+                            const int q = j & 3, t = j >> 2;  // matrices 2 t, 2 t + 1 of the four
+                            *reinterpret_cast<float4 *>(stage + lane * 256 + (((4 * q + 2 * y + t) ^ (lane & 15)) << 4)) =
+                                make_float4(__uint_as_float(v[16 * t + 2 * q]) * inv, __uint_as_float(v[16 * t + 2 * q + 1]) * inv,
+                                            __uint_as_float(v[16 * t + 8 + 2 * q]) * inv, __uint_as_float(v[16 * t + 9 + 2 * q]) * inv);
+                        }
                     }
                     __syncwarp();
 #pragma unroll
@@ -1130,7 +1153,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int row = 2 * (j0 + j) + (lane >> 4);
-                            if (whose >> row & 1u) __stcg(reinterpret_cast<float4 *>(dst + (int64_t)row * CSA2_D + k) + (lane & 15), o[j]);
+                            if (whose >> row & 1u)
+                                __stcg(reinterpret_cast<float4 *>(dst + (int64_t)row * CSA2_D + (k & 128) + 32 * ((lane >> 2) & 3) + (k & 64) / 4) + (lane & 3), o[j]);
                         }
                     }
                     __syncwarp();
