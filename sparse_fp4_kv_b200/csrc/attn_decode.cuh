@@ -285,9 +285,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_decode(DecParams p) {
     pdl_trigger();
     if (warp == kDecResWarp && n > 0) {
         // While the previous kernel finishes: L2 prefetches of what this CTA
-        // reads first and no kernel of this library writes -- q of its
-        // queries and their sequences' page-table rows. A prefetch only warms
-        // L2; every read of them happens after the dependency wait below.
+        // reads first -- q of its queries and their sequences' page-table
+        // rows. A prefetch only warms L2 (a page operator before may still
+        // write there); every read happens after the dependency wait below.
         const int64_t ua = x0 / p.tpq, ub = (x1 - 1) / p.tpq;
         for (int64_t u = ua; u <= ub; ++u) {
             const uint8_t *qb = reinterpret_cast<const uint8_t *>(p.q + u * H * CSA2_D);

@@ -14,7 +14,7 @@
 // group's prefix, or the heads of one query against its own rows (the entries
 // behind the prefix, then its window). A strip's rows of the cache are cut
 // into tiles of 256; all tiles form one list, and every pair of CTAs takes an
-// equal run of it. A run's part of a strip leaves an f32 partial (o divided
+// equal share of it. A share's part of a strip leaves an f32 partial (o divided
 // by its own denominator, and its log-sum-exp); k_prefix_merge joins a
 // query's partials of its prefix strip and of its own.
 //
@@ -32,9 +32,16 @@
 // keys of tile i + 1, then up to four chunks of 64 rows of the values of
 // tile i, so that S of the next tile runs while the softmax of a tile does.
 //
-// Warps: 4 softmax warps (a thread has half a row: 128 scores), 8 that fetch
-// rows two chunks ahead into registers, dequantise them (exact in f16) and
-// store them swizzled, one that issues the products (in the first CTA).
+// Warps: 4 of softmax (a thread has half a row: 128 scores), 16 that fetch rows
+// into registers a group of chunks ahead, dequantise them (exact in f16) and
+// store them, one that issues the products (in the first CTA), one that resolves
+// rows up to four tiles ahead, one that has q copied in.
+//
+// Measured (8 queries x 64 heads on 200,000 shared entries: 3128 tiles): 195 us,
+// 1.08 PFLOP/s. A tile takes 7300 cycles, 4096 of them the tensor pipe's (55 %
+// active); the array of L1 and shared memory is busy 73 % with loads and stores,
+// beside the products' operands. At 1000 W the clock falls to 1.5 - 1.6 GHz, so
+// what is left to gain is work that is not done rather than waits.
 #pragma once
 
 #include "common.cuh"
@@ -103,7 +110,7 @@ constexpr int kPxRows = 128;  // query rows of a strip
 constexpr int kPxSoftWarps = 4;
 constexpr int kPxLoadWarps = 16;
 constexpr int kPxMmaWarp = kPxSoftWarps + kPxLoadWarps;
-constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;  // three idle warps fill the last group of four
+constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;  // products, resolver, q, and one idle warp
 constexpr int kPxSlots = 4;
 constexpr int kPxSlotBytes = 32768;
 constexpr int kPxQBytes = 64 * CSA2_D * 2;
@@ -554,21 +561,17 @@ struct __align__(16) PxInfo {
 //     position 8 m + 2 q + e  <-  value 32 q + 2 m + e   (m < 16, q < 4, e < 2),
 // pair m of lane q's unit being what it stores to matrix m. The products do not
 // mind an order of the latent axis: q is converted in the same one, and the
-// columns of O are put back when a partial is stored. The loads are predicated
-// instructions on registers that nothing else merges into, so none waits for
-// another.
+// columns of O are put back when a partial is stored.
 struct PxRaw {
     uint32_t v[4][4], sc[4];
 };
-__device__ __forceinline__ void px_ld16(uint32_t *v, const void *at, bool take) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
-        : "l"(at), "r"((int)take));
+// Loads into registers that hold something already ("+"): written so, the two
+// branches that fetch (entries, window rows) share the registers, and no move
+// after them waits for a load.
+__device__ __forceinline__ void px_ld16(uint32_t (&v)[4], const void *at) {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]) : "l"(at));
 }
-__device__ __forceinline__ void px_ld4(uint32_t &v, const void *at, bool take) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)take));
-}
+__device__ __forceinline__ void px_ld4(uint32_t &v, const void *at) { asm volatile("ld.global.nc.u32 %0, [%1];" : "+r"(v) : "l"(at)); }
 // Units u0 and u0 + 1 of a run: `row` the lane's, the second unit ROWS rows and
 // VALUES values further on.
 template <int ROWS, int VALUES>
@@ -578,8 +581,8 @@ __device__ __forceinline__ void px_fetch_run(const PrefixParams &p, int64_t row,
     const uint8_t *sc = p.kv.scales + row * (CSA2_D / CSA2_BLOCK) + ((d0 / CSA2_BLOCK) & ~3);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        px_ld16(raw.v[u0 + u], at + u * (ROWS * (CSA2_D / 2) + VALUES / 2), true);
-        px_ld4(raw.sc[u0 + u], sc + u * (ROWS * (CSA2_D / CSA2_BLOCK) + VALUES / CSA2_BLOCK), true);
+        px_ld16(raw.v[u0 + u], at + u * (ROWS * (CSA2_D / 2) + VALUES / 2));
+        px_ld4(raw.sc[u0 + u], sc + u * (ROWS * (CSA2_D / CSA2_BLOCK) + VALUES / CSA2_BLOCK));
     }
 }
 // Four matrices of 8 rows by 16 bytes; lane l gives the address of row l % 8 of
@@ -901,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             } else if (kind == kRunWindow && !skip) {
                 const uint8_t *at = run_of(f);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], at + window_step(u), true);
+                for (int u = 0; u < 4; ++u) px_ld16(raw.v[u], at + window_step(u));
             }
         };
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&info_full[0], 0));
