@@ -1499,12 +1499,9 @@ bool make_q_map(CUtensorMap *tm, uint16_t *q16, int64_t rows) {
 // Pairs of CTAs of the attention kernel that the current device runs at once
 // (asked once per device, after its shared-memory attribute is set).
 int32_t prefix_resident_pairs() {
-    static std::mutex mu;
-    static std::map<int, int> per_dev;
+    static std::atomic<int> known[64];
     const int dev = current_device();
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = per_dev.find(dev);
-    if (it != per_dev.end()) return it->second;
+    if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1521,7 +1518,7 @@ int32_t prefix_resident_pairs() {
         cudaGetLastError();
         return 0;
     }
-    per_dev[dev] = n;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -1648,9 +1645,10 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     csa2_status st = check_kv(kv, false);
     if (st != CSA2_OK) return st;
     if (h < 1 || h > CSA2_PREFIX_MAX_HEADS) return CSA2_ERR_UNSUPPORTED;
-    if (nq <= 0 || nq > 65535 || q_per_seq <= 0 || (nq + q_per_seq - 1) / q_per_seq > kv->batch)
-        return CSA2_ERR_INVALID_ARG;
-    if (n_members < 0 || n_groups < 0 || n_members > (nq + q_per_seq - 1) / q_per_seq || n_groups > n_members ||
+    if (nq <= 0 || nq > 65535 || q_per_seq <= 0) return CSA2_ERR_INVALID_ARG;
+    const int64_t seqs = ((int64_t)nq + q_per_seq - 1) / q_per_seq;
+    if (seqs > kv->batch) return CSA2_ERR_INVALID_ARG;
+    if (n_members < 0 || n_groups < 0 || n_members > seqs || n_groups > n_members ||
         (int64_t)n_members * q_per_seq > kPxMaxQueries)
         return CSA2_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale) || w_max < 0) return CSA2_ERR_INVALID_ARG;

@@ -70,6 +70,7 @@ def test_prefix_attention_refuses_on_the_host(binding):
     assert call(h=0) == 2 and call(h=129) == 2
     assert call(nq=5) == 1 and call(nq=0) == 1 and call(qps=0, wsb=1 << 20) == 1
     assert call(n_members=5) == 1 and call(n_groups=4) == 1 and call(n_members=-1, n_groups=-1) == 1
+    assert call(qps=2**31 - 1, n_members=1, n_groups=1, wsb=1 << 30) == 1  # more queries than a call takes
     assert call(members=None) == 1 and call(begin=None) == 1 and call(prefix=0x3001) == 1
     assert call(q=0x5008) == 1 and call(o=None) == 1 and call(lse=0x4002) == 1
     assert call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
