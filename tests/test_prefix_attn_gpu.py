@@ -302,3 +302,26 @@ def test_empty_groups_and_an_unlisted_batch(B, cuda_device):
     none = torch.empty(0, dtype=torch.int32, device=cuda_device)
     B.csa2_prefix_attn_decode(*c.args[:3], none, torch.zeros(1, dtype=torch.int32, device=cuda_device), none, *c.args[6:13], o, *c.args[14:])
     assert (o == 77.0).all() and B.csa2_device_status() == 0
+
+
+def test_two_graphs_share_a_workspace(B, cuda_device):
+    """Captured calls of different shapes over one workspace, replayed in turn on one stream."""
+    a = Case(cuda_device, [6], [3000], [40], 32, 64, w=16, seed=21)
+    b = Case(cuda_device, [1, 4], [90, 700], [5, 300], 64, 64, seed=22)
+    size = max(B.csa2_prefix_attn_workspace_size(6, 1, 1, 32), B.csa2_prefix_attn_workspace_size(5, 2, 1, 64))
+    ws = B.workspace(size, cuda_device)
+    outs = [c.run(B, ws=ws) for c in (a, b)]
+    torch.cuda.synchronize()
+    graphs = []
+    for c in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.csa2_prefix_attn_decode(*c.args)
+    for x in (*outs[0], *outs[1]):
+        x.fill_(77.0)
+    for i in (0, 1, 1, 0, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    assert B.csa2_device_status() == 0
+    a.check(*outs[0])
+    b.check(*outs[1])
