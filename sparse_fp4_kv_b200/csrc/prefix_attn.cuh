@@ -118,6 +118,13 @@ constexpr int kPxPBytes = 64 * kPxTile * 2;
 constexpr int kPxMisc = 2048;
 constexpr size_t kPxSmem = 1024 + kPxQBytes + kPxPBytes + (size_t)kPxSlots * kPxSlotBytes + kPxMisc;
 constexpr float kPxRescale = 8.0f;  // log2 by which the maximum may rise before O is rescaled
+// Probabilities are f16 (11 bits, which is what the products take), but their sum
+// is f32. In a long list many small ones may weigh more than f16's least number
+// lets through, so they are taken 2^kPxBias times as large: at most 2^15, and one
+// is rounded by at most 2^-32 of the largest (2^-25 without; a million entries at
+// 2^-25.5 of one lost 2 % of the result).
+constexpr float kPxBias = 7.0f;
+static_assert(kPxRescale + kPxBias <= 15.0f, "probabilities stay finite in f16");
 static_assert(kPxSmem <= 232448, "shared memory of one CTA");
 static_assert(kPxSlots == 4 && kPxLoadWarps == 4 * kPxSlots, "a set of four warps a slot");
 
@@ -1060,7 +1067,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                 m_run = top;
                 l_run *= alpha;
             }
-            const float at = m_run == -INFINITY ? 0.0f : m_run;
+            const float at = m_run == -INFINITY ? 0.0f : m_run - kPxBias;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t pk[32];
             auto exps = [&](int k0) {  // scores 32 k0 .. + 63
@@ -1074,7 +1081,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                         const float a = ex2(fmaf(__uint_as_float(v[2 * j]), p.scale_log2, -at));
                         const float b = ex2(fmaf(__uint_as_float(v[2 * j + 1]), p.scale_log2, -at));
                         sum[j & 3] += a + b;
-                        // f16 probabilities: 2^-11 relative, what the products take
+                        // f16: 2^-11 relative, 2^-25 absolute (see kPxBias)
                         const __half2 hh = __floats2half2_rn(a, b);
                         pk[16 * k + j] = *reinterpret_cast<const uint32_t *>(&hh);
                     }
@@ -1163,7 +1170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
                     __syncwarp();
                 }
                 if (mine && half == 0)
-                    (pre ? p.pre_lse : p.own_lse)[part] = l > 0.0f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    (pre ? p.pre_lse : p.own_lse)[part] = l > 0.0f ? (m_run - kPxBias + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 tc_fence_before();
                 m_run = -INFINITY;
                 l_run = 0.0f;

@@ -325,3 +325,37 @@ def test_two_graphs_share_a_workspace(B, cuda_device):
     assert B.csa2_device_status() == 0
     a.check(*outs[0])
     b.check(*outs[1])
+
+
+@pytest.mark.parametrize("n,split", [(200, 200), (256, 256), (5000, 5000), (5000, 0), (5000, 137)])
+@pytest.mark.parametrize("gap", [17.0, 20.0, 23.0, 24.5, 25.5, 27.0])
+def test_weak_weights_count_beside_a_strong_one(B, cuda_device, n, split, gap):
+    """One entry 2^gap times as heavy as each of the others, which alone fill the latent values that it leaves zero.
+    Their weights count in o as they do in lse: rounded to f16 they are off by at most 2^-11, or by 2^-32 of the
+    heaviest one (half a step of f16's least numbers, the probabilities being at least 2^7 at the maximum)."""
+    c = Case(cuda_device, [2], [split], [n - split], 16, 64, seed=int(gap), spare=0, scale=math.log(2))
+    rng = np.random.default_rng(n + int(gap))
+    c.codes &= 0x77  # no signs: nothing cancels
+    c.codes[:, :8] = 0
+    c.scales[:] = 0x38  # 1
+    for s, first in ((int(c.members[0]), int(c.members[0])), (int(c.members[1]), int(c.members[0]))):
+        t = int(rng.integers(0, n)) if split == 0 else 7  # in the prefix it is the first member's
+        at = c.table[first if t < split else s, t // 64] * 64 + t % 64
+        c.codes[at] = 0
+        c.codes[at, :8] = 0x22  # sixteen values of 1
+    c.q[:] = 0
+    c.q[:, :, :16] = gap / 16  # a multiple of 1/32 below 2: exact
+    o, lse = c.run(B)
+    assert B.csa2_device_status() == 0
+    for j in range(2):
+        u = int(c.members[j])
+        q, v = c.q[u].double().numpy(), c.rows(j, u)
+        want, wl, _, tl = ref.attend(q, v, c.scale)
+        s = q @ v.T * c.scale
+        p = np.exp(s - s.max(1, keepdims=True))
+        l = p.sum(1, keepdims=True)
+        es = 512 * 2.0 ** -23 * (np.abs(q) @ np.abs(v).T).max(1) * c.scale + 2.0 ** -21 * (np.abs(s).max(1) + 1)
+        tol = 2.0 ** -8 * np.abs(want) + ((2.0 ** -11 + 2 * es[:, None]) * p @ np.abs(v) + 2.0 ** -32 * np.abs(v).sum(0)) / l * 1.01
+        off = np.abs(o[u].double().cpu().numpy() - want)
+        assert (off <= tol).all(), f"member {j}: {(off / tol).max():.3g} times what it may be"
+        assert (np.abs(lse[u].double().cpu().numpy() - wl) <= tl).all()
