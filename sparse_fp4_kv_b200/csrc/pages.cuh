@@ -64,28 +64,31 @@ struct PagesParams {
 
 __device__ __forceinline__ int32_t pages_of(int32_t len, int32_t ps) { return len / ps + (len % ps != 0); }
 
-// Exclusive sum over the block (kPlanThreads threads) and its total.
-__device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t *warp_sums, int32_t &total) {
+// Exclusive sum over the block (kPlanThreads threads) and its total. T is 64 bits
+// where the sum may pass 32 (what the entries of a call need; counts of pages of
+// the cache stay below 2^26).
+template <class T>
+__device__ __forceinline__ T block_exclusive(T v, T *warp_sums, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t s = v;
+    T s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        const T u = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (lane >= o) s += u;
     }
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int32_t w = warp_sums[lane];
+        T w = warp_sums[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            const T u = __shfl_up_sync(0xFFFFFFFFu, w, o);
             if (lane >= o) w += u;
         }
         warp_sums[lane] = w;
     }
     __syncthreads();
-    const int32_t before = (warp ? warp_sums[warp - 1] : 0) + s - v;
+    const T before = (warp ? warp_sums[warp - 1] : 0) + s - v;
     total = warp_sums[31];
     __syncthreads();
     return before;
@@ -95,6 +98,7 @@ static_assert(kPlanThreads == 1024, "block_exclusive sums 32 warps");
 // What every CTA of the plan tells the others.
 struct PlanShared {
     int32_t warp_sums[32];
+    int64_t need_sums[32];
     int32_t count[2];  // pages of this CTA's run that count (two kinds)
     int32_t total_need;
 };
@@ -335,10 +339,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
             const int32_t i = i0 + threadIdx.x;
             PageEntry e = kRefused;
             if (i < p.n) e = plan_entry<FORK>(p, i);
-            int32_t t;
-            const int32_t before = block_exclusive(e.need, sh.warp_sums, t);
+            int64_t t;
+            const int64_t before = block_exclusive((int64_t)e.need, sh.need_sums, t);
             // a rank above every page number stands for "no page left"
-            e.base = (int32_t)min(sum + before, (int64_t)INT32_MAX - p.kv.max_pages - 1);
+            e.base = (int32_t)min(sum + before, (int64_t)INT32_MAX);
             if (i < p.n) p.entry[i] = e;
             sum += t;
         }

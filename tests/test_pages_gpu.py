@@ -260,3 +260,28 @@ def test_captured_and_replayed(B, cuda_device):
         pool.resize([3, 4, 5], [0, 0, 0])
     torch.cuda.synchronize()
     g.same(pool)
+
+
+def test_needs_that_pass_32_bits_are_refused(B, cuda_device):
+    """Rows of 2^26 pages: what the entries ask for together passes 2^31 pages, and every entry behind the first large
+    one that needs pages is refused."""
+    ps, width, batch, pages = 32, 1 << 26, 40, 12
+    i32 = dict(dtype=torch.int32, device=cuda_device)
+    table = torch.full((batch, width), -1, **i32)
+    seq_len, refs = torch.zeros(batch, **i32), torch.zeros(pages, **i32)
+    table[39, :2], seq_len[39], refs[3], refs[5] = torch.tensor([3, 5], **i32), 64, 1, 1
+    z = lambda w: torch.zeros((pages * ps, w), dtype=torch.uint8, device=cuda_device)
+    kv = B.KvCache(z(256), z(32), None, table, seq_len, ps)
+    ws = B.workspace(B.csa2_pages_workspace_size(batch, batch, pages), cuda_device)
+    most = 2 ** 31 - 1
+    seq = torch.tensor([1, *range(2, 37), 37, 39, 38], **i32)
+    new = torch.tensor([70, *[most] * 35, 1, 20, 64], **i32)
+    src, dst = (torch.full((len(seq),), -7, **i32) for _ in range(2))
+    B.csa2_pages_resize(kv, refs, seq, new, src, dst, ws)
+    assert B.csa2_device_status() == PAGES
+    assert table[1, :4].tolist() == [0, 1, 2, -1] and table[39, :3].tolist() == [3, -1, -1]
+    assert refs.tolist() == [1, 1, 1, 1] + [0] * 8
+    want = torch.zeros(batch, **i32)
+    want[1], want[39] = 70, 20
+    assert torch.equal(seq_len, want) and (src == -1).all() and (dst == -1).all()
+    assert int((table >= 0).sum()) == 4
