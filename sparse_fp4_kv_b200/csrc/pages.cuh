@@ -223,8 +223,9 @@ __device__ __forceinline__ void pages_apply(const PagesParams &p, int32_t t0, in
         const int32_t into = part ? p.fresh[e.base] : -1;
         if (FORK) {
             const int32_t *src = p.table + (int64_t)p.from[i] * width;
-            const int32_t whole = e.length / ps;
-            for (int32_t c = t0; c < width; c += step) {
+            const uint32_t whole = (uint32_t)(e.length / ps);
+            // unsigned: the last step may pass 2^31 in the widest rows
+            for (uint32_t c = t0; c < (uint32_t)width; c += step) {
                 int32_t page = -1;
                 if (c < whole) {
                     page = src[c];

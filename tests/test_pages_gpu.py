@@ -285,3 +285,29 @@ def test_needs_that_pass_32_bits_are_refused(B, cuda_device):
     want[1], want[39] = 70, 20
     assert torch.equal(seq_len, want) and (src == -1).all() and (dst == -1).all()
     assert int((table >= 0).sum()) == 4
+
+
+def test_rows_as_wide_as_32_bits(B, cuda_device):
+    """A fork and its release in rows of 2^31 - 1 columns."""
+    ps, width, pages = 64, 2 ** 31 - 1, 9
+    i32 = dict(dtype=torch.int32, device=cuda_device)
+    table = torch.full((2, width), -1, **i32)
+    table[0, :3] = torch.tensor([7, 2, 4], **i32)
+    seq_len, refs = torch.tensor([150, 0], **i32), torch.zeros(pages, **i32)
+    refs[[7, 2, 4]] = 1
+    z = lambda w: torch.zeros((pages * ps, w), dtype=torch.uint8, device=cuda_device)
+    kv = B.KvCache(z(256), z(32), None, table, seq_len, ps)
+    ws = B.workspace(B.csa2_pages_workspace_size(1, 2, pages), cuda_device)
+    one = lambda x: torch.tensor([x], **i32)
+    B.csa2_pages_fork(kv, refs, one(0), one(1), None, None, None, ws)
+    assert B.csa2_device_status() == 0
+    assert table[1, :4].tolist() == [7, 2, 0, -1] and seq_len.tolist() == [150, 150]
+    assert refs.tolist() == [1, 0, 2, 0, 1, 0, 0, 2, 0]
+    assert int(table[1].max()) == 7 and int((table[1, 3:] != -1).sum()) == 0 and int((table[0, 3:] != -1).sum()) == 0
+    B.csa2_pages_resize(kv, refs, one(1), one(0), None, None, ws)
+    assert B.csa2_device_status() == 0
+    assert refs.tolist() == [0, 0, 1, 0, 1, 0, 0, 1, 0] and int((table[1] != -1).sum()) == 0
+    live, (src, dst) = one(-1), (torch.full((pages // 2,), -7, **i32) for _ in range(2))
+    B.csa2_pages_compact(kv, refs, src, dst, live, ws)
+    # live are 2, 4 and 7: 4 moves to 0 and 7 to 1
+    assert B.csa2_device_status() == 0 and int(live) == 3 and table[0, :4].tolist() == [1, 2, 0, -1]
