@@ -1017,6 +1017,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPxThreads, 1) k_pre
             // where the strip's partial goes (used when last)
             const bool pre = w.t.member0 >= 0;
             const int64_t part = pre ? ((int64_t)c + w.s) * kPxRows + 64 * rank + r : ((int64_t)c + (w.s - w.n_pre)) * p.h + 64 * rank + r;
+            // what the resolver tells of the tile is read below: S being done does not
+            // order its plain stores before that (told long before S: no time is lost)
+            if (ok) ok = mbar_wait(&info_full[i % kPxInfos], (uint32_t)(i / kPxInfos) & 1u);
             if (ok) ok = mbar_wait(&s_full[i & 1], ((uint32_t)i >> 1) & 1u);
             tc_fence_after();
             if (i + 1 < n) {
