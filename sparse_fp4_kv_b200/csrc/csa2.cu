@@ -1522,18 +1522,42 @@ int32_t prefix_resident_pairs() {
     return n;
 }
 
-// Whether the plan's cluster applies as well: up to kFuseCells table cells and
-// kFuseRows rows to move, eight of each for a thread or a warp of the cluster.
-constexpr int64_t kFuseCells = 8 * kPlanCtas * kPlanThreads, kFuseRows = 8 * kPlanCtas * (kPlanThreads / 32) * kCopyUnitRows;
+// Threads (log2) of the plan's cluster that serve one entry when the cluster applies
+// what it planned: up to all of them for one entry, 128 (four warps) from 64 entries
+// on, and no more than a thread for each column and a warp for each unit to copy
+// (one row of 64 columns freed: 6.5 us inside a graph, 6.9 with all threads at it).
+// -1: the apply launch does, which is the faster form once a thread walks more than
+// four columns, or a warp copies more than one unit, one after the other. Calls
+// from the host, cluster against apply launch, us:
+//   1, 2, 4, 8 columns a thread (one row of 8192 ... 65,536 columns, shared by a
+//     fork and freed): 10.4, 10.4, 11.8, 14.4 against 12.4, and 10.4, 12.4, 12.4,
+//     16.5 against 12.5 to 14.4
+//   1, 2, 4 units a warp (a page of 2048 ... 8192 rows copied by a fork): 12.4,
+//     14.2, 17.2 against 12.5; 64 forks with pages of 32, 64, 128 rows the same
+// (inside a graph both forms take 7 to 10 us up to these limits). A resize copies
+// only where it cuts a shared page, and may have two units: a step of 64 sequences
+// in pages of 64 rows takes 10.4 against 12.4, or 14.4 should it copy them all.
+constexpr int64_t kFuseCells = 4, kFuseForkUnits = 1, kFuseResizeUnits = 2;
+int32_t fuse_group_log2(int32_t n, int64_t max_pages, int64_t page_size, int64_t max_units) {
+    constexpr int64_t all = kPlanCtas * kPlanThreads;
+    static_assert(all == 1 << 13, "log2 of the cluster's threads");
+    const int64_t work = std::max(max_pages, 32 * (page_size / kCopyUnitRows));
+    int32_t log2 = 13;
+    while (log2 > 7 && (((int64_t)n << log2) > all || (1ll << (log2 - 1)) >= work)) --log2;
+    const int64_t g = 1ll << log2, turns = (n * g + all - 1) / all;
+    const auto rounds = [&](int64_t x, int64_t at_once) { return turns * ((x + at_once - 1) / at_once); };
+    const bool few = rounds(max_pages, g) <= kFuseCells && rounds(page_size / kCopyUnitRows, g / 32) <= max_units;
+    return few ? log2 : -1;
+}
 
 template <bool FORK>
 csa2_status pages_run(PagesParams &p, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const csa2_status st = pages_workspace(p, ws, ws_bytes);
     if (st != CSA2_OK) return st;
-    p.fused = (int64_t)p.n * p.kv.max_pages <= kFuseCells && (int64_t)p.n * p.kv.page_size <= kFuseRows;
+    p.group_log2 = fuse_group_log2(p.n, p.kv.max_pages, p.kv.page_size, FORK ? kFuseForkUnits : kFuseResizeUnits);
     launch_cluster(k_pages_plan<FORK>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream, kPlanCtas, p);
     if (check_launch() != CSA2_OK) return CSA2_ERR_CUDA;
-    if (p.fused) return CSA2_OK;
+    if (p.group_log2 >= 0) return CSA2_OK;
     // along x: enough blocks for the longest row at four columns a thread and
     // for a page copy, but no more than fill the machine with all entries
     const int64_t cols = ((int64_t)p.kv.max_pages + 4 * kApplyThreads - 1) / (4 * kApplyThreads);

@@ -49,7 +49,7 @@ struct PagesParams {
     csa2_kv_desc kv;
     int32_t *table, *seq_len, *refs;
     int32_t num_pages, n;
-    int32_t fused;  // the plan's cluster applies what it planned
+    int32_t group_log2;  // log2 of the plan's threads for an entry, where it applies what it planned; -1: the apply launch does
     const int32_t *from;    // fork: parents
     const int32_t *to;      // fork: children; resize: sequences
     const int32_t *length;  // fork: entries to share (nullable); resize: new lengths
@@ -384,10 +384,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
         before += t;
     }
     cluster_wait();  // no CTA leaves while another reads its shared memory
-    if (p.fused) {
+    if (p.group_log2 >= 0) {
         cluster_sync_all();  // the plan is in place
-        constexpr int kGroup = 128;  // threads an entry
-        pages_apply<FORK>(p, threadIdx.x % kGroup, kGroup, rank * (kPlanThreads / kGroup) + threadIdx.x / kGroup, kPlanCtas * (kPlanThreads / kGroup));
+        const int32_t t = rank * kPlanThreads + threadIdx.x, group = 1 << p.group_log2;
+        pages_apply<FORK>(p, t & (group - 1), group, t >> p.group_log2, (kPlanCtas * kPlanThreads) >> p.group_log2);
     }
 }
 

@@ -311,3 +311,23 @@ def test_rows_as_wide_as_32_bits(B, cuda_device):
     B.csa2_pages_compact(kv, refs, src, dst, live, ws)
     # live are 2, 4 and 7: 4 moves to 0 and 7 to 1
     assert B.csa2_device_status() == 0 and int(live) == 3 and table[0, :4].tolist() == [1, 2, 0, -1]
+
+
+@pytest.mark.parametrize("n,ps,width", [(1, 32, 8000), (1, 32, 70000), (1, 16384, 4), (1, 65536, 4), (2, 64, 20000), (5, 32, 6000), (3, 4096, 5)])
+def test_wide_rows_and_large_pages(B, cuda_device, n, ps, width):
+    """Few entries with long rows of the table or large partial pages: forked, grown, rolled back and freed."""
+    rng = np.random.default_rng(n * ps + width)
+    long = (width - 1) * ps - 5 if ps * width < 400_000 else min(width - 3, 900) * ps - 5
+    pages = -(-long // ps) + (3 * n + 4 if ps > 1000 else 300)
+    pool = Pool(rng, pages, ps, 64 if ps > 1000 else 0, n + 2, width)
+    pool.fill(rng, [long])
+    g = Gpu(B, pool, cuda_device)
+    child = [1 + i for i in range(n)]
+    lens = [long - i * (ps // 2 + 1) for i in range(n)]
+    _pair(g.fork([0] * n, child, lens), pool.fork([0] * n, child, lens))
+    g.same(pool)
+    room = width * ps
+    for new in ([min(room, int(x) + ps) for x in pool.seq_len[child]], [int(x) // 2 + 1 for x in lens], [min(room, 200 * ps // n)] * n, [0] * n):
+        pool.refused = False
+        _pair(g.resize(child, new), pool.resize(child, new))
+        g.same(pool, PAGES if pool.refused else 0)
