@@ -64,31 +64,30 @@ struct PagesParams {
 
 __device__ __forceinline__ int32_t pages_of(int32_t len, int32_t ps) { return len / ps + (len % ps != 0); }
 
-// Exclusive sum over the block (kPlanThreads threads) and its total. T is 64 bits
-// where the sum may pass 32 (what the entries of a call need; counts of pages of
-// the cache stay below 2^26).
-template <class T>
-__device__ __forceinline__ T block_exclusive(T v, T *warp_sums, T &total) {
+// Exclusive sum over the block (kPlanThreads threads) and its total. A warp's sum is
+// cut at `cap`: summands and cap of up to 2^26 (pages of a cache, and one more)
+// keep every sum below 2^32, a result up to cap is exact, and one above stays above.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t &total, uint32_t cap = 0xFFFFFFFFu) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T s = v;
+    uint32_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (lane >= o) s += u;
     }
-    if (lane == 31) warp_sums[warp] = s;
+    if (lane == 31) warp_sums[warp] = min(s, cap);
     __syncthreads();
     if (warp == 0) {
-        T w = warp_sums[lane];
+        uint32_t w = warp_sums[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const T u = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
             if (lane >= o) w += u;
         }
         warp_sums[lane] = w;
     }
     __syncthreads();
-    const T before = (warp ? warp_sums[warp - 1] : 0) + s - v;
+    const uint32_t before = (warp ? warp_sums[warp - 1] : 0) + s - v;
     total = warp_sums[31];
     __syncthreads();
     return before;
@@ -97,8 +96,7 @@ static_assert(kPlanThreads == 1024, "block_exclusive sums 32 warps");
 
 // What every CTA of the plan tells the others.
 struct PlanShared {
-    int32_t warp_sums[32];
-    int64_t need_sums[32];
+    uint32_t warp_sums[32];
     int32_t count[2];  // pages of this CTA's run that count (two kinds)
     int32_t total_need;
 };
@@ -340,10 +338,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
             const int32_t i = i0 + threadIdx.x;
             PageEntry e = kRefused;
             if (i < p.n) e = plan_entry<FORK>(p, i);
-            int64_t t;
-            const int64_t before = block_exclusive((int64_t)e.need, sh.need_sums, t);
-            // a rank above every page number stands for "no page left"
-            e.base = (int32_t)min(sum + before, (int64_t)INT32_MAX);
+            uint32_t t;
+            const uint32_t cap = (uint32_t)p.num_pages + 1;  // a need or a rank that no cache serves
+            e.need = (int32_t)min((uint32_t)e.need, cap);
+            const uint32_t before = block_exclusive((uint32_t)e.need, sh.warp_sums, t, cap);
+            e.base = (int32_t)min(sum + before, (int64_t)cap);
             if (i < p.n) p.entry[i] = e;
             sum += t;
         }
@@ -357,9 +356,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
         const int4 r = plan_refs(p.refs, plan_page(lo, k), hi);
         mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     }
-    int32_t total;
+    uint32_t total;
     block_exclusive(mine, sh.warp_sums, total);
-    if (threadIdx.x == 0) sh.count[0] = total;
+    if (threadIdx.x == 0) sh.count[0] = (int32_t)total;
     cluster_sync_all();
     int32_t before, all;
     cluster_sums(sh, 0, rank, before, all);
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PagesParams p) {
         const int32_t page = plan_page(lo, k);
         const int4 r = plan_refs(p.refs, page, hi);
         const int32_t f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
-        int32_t t;
+        uint32_t t;
         int32_t at = before + block_exclusive(f[0] + f[1] + f[2] + f[3], sh.warp_sums, t);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -427,13 +426,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact_plan(PagesParams
     const int32_t run = ((p.num_pages + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
     const int32_t lo = min((int64_t)p.num_pages, (int64_t)rank * run), hi = min((int64_t)p.num_pages, (int64_t)lo + run);
     const int32_t rounds = (hi - lo + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    int32_t mine = 0, total;
+    int32_t mine = 0;
+    uint32_t total;
     for (int32_t k = 0; k < rounds; ++k) {
         const int4 r = plan_refs(p.refs, plan_page(lo, k), hi);
         mine += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
     }
     block_exclusive(mine, sh.warp_sums, total);
-    if (threadIdx.x == 0) sh.count[0] = total;
+    if (threadIdx.x == 0) sh.count[0] = (int32_t)total;
     cluster_sync_all();
     int32_t live_before, live;
     cluster_sums(sh, 0, rank, live_before, live);
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact_plan(PagesParams
         for (int j = 0; j < 4; ++j) mine += page + j < min(hi, live) && v[j] <= 0;
     }
     block_exclusive(mine, sh.warp_sums, total);
-    if (threadIdx.x == 0) sh.count[1] = total;
+    if (threadIdx.x == 0) sh.count[1] = (int32_t)total;
     cluster_sync_all();
     int32_t hole_before, holes;
     cluster_sums(sh, 1, rank, hole_before, holes);
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact_plan(PagesParams
         const int32_t page = plan_page(lo, k);
         const int4 r = plan_refs(p.refs, page, hi);
         const int32_t v[4] = {r.x, r.y, r.z, r.w};
-        int32_t t;
+        uint32_t t;
         int32_t at = before + block_exclusive((v[0] > 0) + (v[1] > 0) + (v[2] > 0) + (v[3] > 0), sh.warp_sums, t);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
