@@ -382,9 +382,9 @@ size_t csa2_pages_workspace_size(int32_t n, int32_t batch, int64_t num_pages);
  * query of the group sees have to be finite, as csa2_append_fp4 writes them.
  * Arithmetic and the range of q are those of csa2_sparse_attn_decode, with
  * probabilities in f16 that are off by at most 2^-11, or by 2^-32 of the
- * largest one. n_groups
- * = 0 is a no-op; at most 2^17 queries (n_members * q_per_seq), n_groups
- * <= n_members <= ceil(nq / q_per_seq), w_max and swa_seq_stride below 2^30.
+ * largest one. n_groups = 0 is a no-op; at most 2^17 listed queries (n_members
+ * * q_per_seq), n_groups <= n_members <= ceil(nq / q_per_seq), w_max and
+ * swa_seq_stride below 2^30.
  * ws: at least csa2_prefix_attn_workspace_size(n_members, n_groups,
  * q_per_seq, h) bytes, whatever the lengths.
  */

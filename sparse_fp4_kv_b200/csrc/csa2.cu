@@ -1669,7 +1669,7 @@ csa2_status csa2_prefix_attn_decode(const void *q_bf16, int32_t nq, int32_t q_pe
     csa2_status st = check_kv(kv, false);
     if (st != CSA2_OK) return st;
     if (h < 1 || h > CSA2_PREFIX_MAX_HEADS) return CSA2_ERR_UNSUPPORTED;
-    if (nq <= 0 || nq > 65535 || q_per_seq <= 0) return CSA2_ERR_INVALID_ARG;
+    if (nq <= 0 || q_per_seq <= 0) return CSA2_ERR_INVALID_ARG;
     const int64_t seqs = ((int64_t)nq + q_per_seq - 1) / q_per_seq;
     if (seqs > kv->batch) return CSA2_ERR_INVALID_ARG;
     if (n_members < 0 || n_groups < 0 || n_members > seqs || n_groups > n_members ||

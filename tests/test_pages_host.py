@@ -94,3 +94,18 @@ def test_page_model_keeps_counts(binding):
     held = np.bincount(pool.table[pool.table >= 0], minlength=60)
     np.testing.assert_array_equal(held, pool.refs)
     assert not pool.refused and (pool.refs[int((pool.refs > 0).sum()):] == 0).all()
+
+
+def test_prefix_attention_takes_up_to_2_17_listed_queries(binding):
+    """The limit is on the listed queries; the check of the workspace comes behind it (nothing is launched)."""
+    f = binding._lib.csa2_prefix_attn_decode
+
+    def call(nq, qps, n_members):
+        return f(0x5000, nq, qps, 2, _desc(binding, batch=1 << 20), 0x1000, n_members, 0x2000, 0x3000, 1, None, None, 0, None, None, 0, 0.1,
+                 0x4000, None, 0x10000, 16, None)
+
+    assert call(65535, 1, 65535) == 3 and call(65536, 1, 65536) == 3 and call(1 << 17, 1, 1 << 17) == 3
+    assert call(70002, 35001, 2) == 3 and call(1 << 20, 1, 7) == 3
+    assert call((1 << 17) + 1, 1, (1 << 17) + 1) == 1 and call(1 << 20, 1 << 16, 3) == 1
+    assert binding.csa2_prefix_attn_workspace_size(1 << 17, 1, 1, 2) > 0
+    assert binding.csa2_prefix_attn_workspace_size((1 << 17) + 1, 1, 1, 2) == 0

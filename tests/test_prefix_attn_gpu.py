@@ -359,3 +359,17 @@ def test_weak_weights_count_beside_a_strong_one(B, cuda_device, n, split, gap):
         off = np.abs(o[u].double().cpu().numpy() - want)
         assert (off <= tol).all(), f"member {j}: {(off / tol).max():.3g} times what it may be"
         assert (np.abs(lse[u].double().cpu().numpy() - wl) <= tl).all()
+
+
+def test_more_than_65535_queries(B, cuda_device):
+    """Two sequences with 35,001 queries each, each with a limit of its own."""
+    c = Case(cuda_device, [2], [70], [30, 5], 2, 32, qps=35001, seed=23, spare=0, limits=lambda rng, n: int(rng.integers(0, n + 1)))
+    o, lse = c.run(B)
+    assert B.csa2_device_status() == 0
+    for j in range(2):
+        for u in range(int(c.members[j]) * c.qps, (int(c.members[j]) + 1) * c.qps, 1009):
+            want, wl, tol, tl = ref.attend(c.q[u].double().numpy(), c.rows(j, u), c.scale)
+            assert (np.abs(o[u].double().cpu().numpy() - want) <= tol).all()
+            got = lse[u].double().cpu().numpy()
+            assert (got == wl).all() if np.isinf(wl).any() else (np.abs(got - wl) <= tl).all()
+    assert not (o == 77.0).all(-1).any()
