@@ -400,20 +400,31 @@ __global__ void __launch_bounds__(kApplyThreads) k_pages_compact_apply(PagesPara
     pdl_trigger();
     pdl_wait();
     const int32_t live = __ldcg(p.head), moves = __ldcg(p.head + 1);
-    if (moves == 0) return;
     const int64_t t0 = (int64_t)blockIdx.x * kApplyThreads + threadIdx.x, step = (int64_t)gridDim.x * kApplyThreads;
     for (int64_t r = t0; r < moves; r += step) {
         const int32_t a = __ldcg(p.copy_src + r);
         p.refs[__ldcg(p.copy_dst + r)] = p.refs[a];
         p.refs[a] = 0;
     }
-    // a sequence's pages end with its length; what lies behind is left alone
-    const int32_t width = p.kv.max_pages;
-    for (int64_t c = t0; c < (int64_t)p.kv.batch * width; c += step) {
-        const int32_t page = p.table[c];
-        if (page < live || page >= p.num_pages) continue;
-        const int32_t b = (int32_t)(c / width);
-        if (c - (int64_t)b * width < pages_of(max(0, p.seq_len[b]), p.kv.page_size)) p.table[c] = __ldcg(p.fresh + page);
+    // a sequence's pages end with its length; what lies behind is left alone. A
+    // warp takes kRowPiece columns of a row at a time.
+    constexpr int kRowPiece = 128;
+    const int32_t width = p.kv.max_pages, lane = threadIdx.x & 31;
+    const int64_t pieces = ((int64_t)width + kRowPiece - 1) / kRowPiece;
+    for (int64_t u = t0 >> 5; u < p.kv.batch * pieces; u += step >> 5) {
+        const int64_t b = u / pieces, c0 = (u - b * pieces) * kRowPiece + lane;
+        int32_t *row = p.table + b * width;
+        int32_t page[kRowPiece / 32];
+#pragma unroll
+        for (int j = 0; j < kRowPiece / 32; ++j) page[j] = c0 + 32 * j < width ? row[c0 + 32 * j] : 0;
+        const int32_t held = pages_of(max(0, p.seq_len[b]), p.kv.page_size);
+#pragma unroll
+        for (int j = 0; j < kRowPiece / 32; ++j) {
+            const int64_t c = c0 + 32 * j;
+            if (c >= min(held, width) || (page[j] >= 0 && page[j] < live)) continue;
+            if (page[j] < 0 || page[j] >= p.num_pages) set_error(CSA2_DEVERR_BAD_ROW);
+            else row[c] = __ldcg(p.fresh + page[j]);
+        }
     }
     copy_pages(p.kv, p.copy_src, p.copy_dst, moves, p.num_pages);
 }

@@ -331,3 +331,26 @@ def test_wide_rows_and_large_pages(B, cuda_device, n, ps, width):
         pool.refused = False
         _pair(g.resize(child, new), pool.resize(child, new))
         g.same(pool, PAGES if pool.refused else 0)
+
+
+def test_compaction_reports_entries_outside_the_cache(B, cuda_device):
+    """Within a sequence's length a page that is none is reported and left as it is, with or without moves; what lies
+    behind the length is not looked at."""
+    rng = np.random.default_rng(8)
+    for holes in (True, False):
+        for bad in (-1, -7, 24, 2 ** 31 - 1, None):
+            pool = Pool(rng, 24, 32, 64, 4, 6)
+            pool.fill(rng, [130, 64, 96], shuffle=holes)
+            pool.table[1, 4] = 99  # behind its two pages
+            if bad is not None:
+                pool.table[2, 1], keep = bad, pool.table[2, 1]
+            g = Gpu(B, pool, cuda_device)
+            if bad is not None:
+                pool.table[2, 1] = keep
+            moves, live = pool.compact()
+            if bad is not None:
+                pool.table[2, 1] = bad
+            got, n_live = g.compact(pool.pages)
+            _pair(got, moves)
+            assert int(n_live) == live
+            g.same(pool, BAD_ROW if bad is not None else 0)
