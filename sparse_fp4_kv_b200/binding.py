@@ -2,7 +2,9 @@
 
 Argument marshalling only: torch tensors are turned into device pointers and
 sizes, the caller's current CUDA stream is passed along, and a non-OK status
-raises. Every step of the computation runs in the library's kernels; there is
+raises. The page operators and the attention over shared prefixes refuse lists,
+tables and outputs of another type or too short, which the C ABI cannot see.
+Every step of the computation runs in the library's kernels; there is
 no fallback of any kind. If the library is missing the import fails.
 """
 import ctypes
@@ -18,6 +20,9 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is not built; run `python -m sparse_fp4_kv_b200.build` (nvcc, sm_100a)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+_INT32 = torch.int32
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 CSA2_D = 512
 CSA2_ATTN_STATIC_SCRATCH_BYTES = 16 << 20
@@ -103,11 +108,28 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _ints(t, n, what):
+    """The address of a list of at least n int32 values (None: null)."""
+    if t is None:
+        return None
+    if t.dtype is _INT32 and t.numel() >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _refused(t, _INT32, n, what)
+
+
+def _refused(t, dtype, n, what):
+    """Raises what is wrong with a tensor that should hold n values of dtype on the device."""
+    if t.dtype is not dtype or t.numel() < n:
+        raise ValueError(f"{what}: at least {n} values of {dtype} expected, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    # the current stream's handle without building a Stream object (4.6 us a call, as long as a small kernel)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the current stream's handle without building a Stream object (4.6 us a call, as long as a small kernel); a
+    # tensor on the device has initialised CUDA
+    return _raw_stream(_current_device())
 
 
 def _check(call, st):
@@ -139,6 +161,23 @@ class KvCache:
         d.contents.max_pages = page_table.shape[1]
         d.contents.batch = page_table.shape[0]
         self.desc = d
+        rows, batch = codes.shape[0], page_table.shape[0]
+        self.num_pages = rows // self.page_size if self.page_size > 0 else 0
+        # what keeps the page operators from writing this cache (None: nothing)
+        self.unwritable = None
+        for name, t, n in (("codes", codes, rows * CSA2_D // 2), ("scales", scales, rows * CSA2_D // 16),
+                           ("kidx", kidx, rows * self.di)):
+            if t is not None and t.numel() * t.element_size() < n:
+                self.unwritable = f"{name}: {n} bytes expected for {rows} rows, got {t.numel() * t.element_size()}"
+        for name, t, n in (("page_table", page_table, page_table.numel()), ("seq_len", seq_len, batch)):
+            if t.dtype is not torch.int32 or t.numel() < n:
+                self.unwritable = f"{name}: at least {n} int32 values expected, got {t.numel()} of {t.dtype}"
+
+    def written(self):
+        """The descriptor, for a call that writes tables, lengths and rows."""
+        if self.unwritable is not None:
+            raise ValueError(self.unwritable)
+        return self.desc
 
     @property
     def di(self):
@@ -232,7 +271,7 @@ def csa2_append_kidx_e4m3(x_bf16, seq, pos, kv: KvCache, stream=None):
 
 
 def _bytes(ws):
-    return ws.numel() * ws.element_size() if ws is not None else 0
+    return ws.nbytes if ws is not None else 0
 
 
 def csa2_pages_workspace_size(n, batch, num_pages):
@@ -241,27 +280,33 @@ def csa2_pages_workspace_size(n, batch, num_pages):
 
 def csa2_pages_copy(kv: KvCache, src, dst, stream=None):
     """Pages src[i] -> dst[i] (codes, scales, keys); -1 is an empty slot."""
-    _check("csa2_pages_copy", _lib.csa2_pages_copy(kv.desc, _ptr(src), _ptr(dst), src.shape[0], _stream(stream)))
+    n = src.numel()
+    _check("csa2_pages_copy", _lib.csa2_pages_copy(kv.written(), _ints(src, n, "src"), _ints(dst, n, "dst"), n, _stream(stream)))
 
 
 def csa2_pages_fork(kv: KvCache, refs, parent, child, length, copy_src, copy_dst, ws, stream=None):
     """Empty sequences child[i] become the first length[i] entries (None: all) of parent[i], sharing whole pages."""
+    n = parent.numel()
     _check("csa2_pages_fork", _lib.csa2_pages_fork(
-        kv.desc, _ptr(refs), _ptr(parent), _ptr(child), _ptr(length), parent.shape[0], _ptr(copy_src), _ptr(copy_dst),
-        _ptr(ws), _bytes(ws), _stream(stream)))
+        kv.written(), _ints(refs, kv.num_pages, "refs"), _ints(parent, n, "parent"), _ints(child, n, "child"),
+        _ints(length, n, "length"), n, _ints(copy_src, n, "copy_src"), _ints(copy_dst, n, "copy_dst"), _ptr(ws), _bytes(ws),
+        _stream(stream)))
 
 
 def csa2_pages_resize(kv: KvCache, refs, seq, new_len, copy_src, copy_dst, ws, stream=None):
     """seq[i] gets new_len[i] entries: pages are released or taken, 0 frees the sequence."""
+    n = seq.numel()
     _check("csa2_pages_resize", _lib.csa2_pages_resize(
-        kv.desc, _ptr(refs), _ptr(seq), _ptr(new_len), seq.shape[0], _ptr(copy_src), _ptr(copy_dst), _ptr(ws),
-        _bytes(ws), _stream(stream)))
+        kv.written(), _ints(refs, kv.num_pages, "refs"), _ints(seq, n, "seq"), _ints(new_len, n, "new_len"), n,
+        _ints(copy_src, n, "copy_src"), _ints(copy_dst, n, "copy_dst"), _ptr(ws), _bytes(ws), _stream(stream)))
 
 
 def csa2_pages_compact(kv: KvCache, refs, move_src, move_dst, n_live, ws, stream=None):
     """Live pages move into the lowest page numbers; the moves go to move_src / move_dst (then -1)."""
+    moves = kv.num_pages // 2
     _check("csa2_pages_compact", _lib.csa2_pages_compact(
-        kv.desc, _ptr(refs), _ptr(move_src), _ptr(move_dst), _ptr(n_live), _ptr(ws), _bytes(ws), _stream(stream)))
+        kv.written(), _ints(refs, kv.num_pages, "refs"), _ints(move_src, moves, "move_src"), _ints(move_dst, moves, "move_dst"),
+        _ints(n_live, 1, "n_live"), _ptr(ws), _bytes(ws), _stream(stream)))
 
 
 def csa2_prefix_attn_workspace_size(n_members, n_groups, q_per_seq, h):
@@ -272,10 +317,20 @@ def csa2_prefix_attn_decode(q_bf16, q_per_seq, kv: KvCache, members, group_begin
                             swa_begin, swa_end, w_max, softmax_scale, o_bf16, lse, ws, stream=None):
     """Attention over whole sequences and their windows, each group's first prefix_len entries read once for all of it."""
     nq, h = q_bf16.shape[0], q_bf16.shape[1]
+    n_groups, n = prefix_len.shape[0], nq * h * CSA2_D
+    for t, name in ((q_bf16, "q_bf16"), (o_bf16, "o_bf16")):
+        if t.dtype is not torch.bfloat16 or t.numel() < n:
+            _refused(t, torch.bfloat16, n, name)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() < nq * h):
+        _refused(lse, torch.float32, nq * h, "lse")
+    if swa is not None and q_per_seq > 0 and _bytes(swa) < -(-nq // q_per_seq) * int(swa_seq_stride) * CSA2_D:
+        raise ValueError(f"swa: {_bytes(swa)} bytes are not {int(swa_seq_stride)} rows for each sequence")
     _check("csa2_prefix_attn_decode", _lib.csa2_prefix_attn_decode(
-        _ptr(q_bf16), nq, q_per_seq, h, kv.desc, _ptr(members), members.shape[0], _ptr(group_begin), _ptr(prefix_len),
-        prefix_len.shape[0], _ptr(q_limit), _ptr(swa), int(swa_seq_stride), _ptr(swa_begin), _ptr(swa_end), int(w_max),
-        float(softmax_scale), _ptr(o_bf16), _ptr(lse), _ptr(ws), _bytes(ws), _stream(stream)))
+        _ptr(q_bf16), nq, q_per_seq, h, kv.desc, _ints(members, 0, "members"), members.shape[0],
+        _ints(group_begin, n_groups + 1, "group_begin"), _ints(prefix_len, n_groups, "prefix_len"), n_groups,
+        _ints(q_limit, nq, "q_limit"), _ptr(swa), int(swa_seq_stride), _ints(swa_begin, nq, "swa_begin"),
+        _ints(swa_end, nq, "swa_end"), int(w_max), float(softmax_scale), _ptr(o_bf16), _ptr(lse), _ptr(ws), _bytes(ws),
+        _stream(stream)))
 
 
 def csa2_score_ids(qidx, w, q_per_seq, ids, kv: KvCache, id_offset, keys, stream=None):

@@ -109,3 +109,99 @@ def test_prefix_attention_takes_up_to_2_17_listed_queries(binding):
     assert call((1 << 17) + 1, 1, (1 << 17) + 1) == 1 and call(1 << 20, 1 << 16, 3) == 1
     assert binding.csa2_prefix_attn_workspace_size(1 << 17, 1, 1, 2) > 0
     assert binding.csa2_prefix_attn_workspace_size((1 << 17) + 1, 1, 1, 2) == 0
+
+
+class _Tensor:
+    """What the binding asks of a device tensor, without a device."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=None):
+        import torch
+        self.shape, self.dtype = shape, dtype or torch.int32
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.element_size()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+@pytest.fixture
+def calls(binding, monkeypatch):
+    """The names of the library's calls that the binding makes; none of them runs."""
+    made = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: made.append(name) or 0
+
+    monkeypatch.setattr(binding, "_lib", Lib())
+    monkeypatch.setattr(binding, "_stream", lambda stream: None)
+    return made
+
+
+def test_the_binding_checks_lists_and_tables(binding, calls):
+    import torch
+    u8, i64 = torch.uint8, torch.int64
+    T = _Tensor
+
+    def cache(rows=4 * 64, scales=None, keys=None, table=None, lens=None):
+        return binding.KvCache(T(rows, 256, dtype=u8), scales or T(rows, 32, dtype=u8), keys or T(rows, 64, dtype=u8), table or T(3, 8),
+                               lens or T(3), 64)
+
+    kv, ws = cache(), T(4096, dtype=u8)
+    # of each call: fine arguments (n = 5, 4 pages) and which of them have a least length of their own
+    copy, fork, resize, compact = (getattr(binding, "csa2_pages_" + x) for x in ("copy", "fork", "resize", "compact"))
+    table = [(copy, [kv, T(5), T(5)], [2]), (fork, [kv, T(4), T(5), T(5), T(5), T(5), T(5), ws], [1, 3, 4, 5, 6]),
+             (resize, [kv, T(4), T(5), T(5), T(5), T(5), ws], [1, 3, 4, 5]), (compact, [kv, T(4), T(2), T(2), T(1), ws], [1, 2, 3, 4])]
+    for f, args, _ in table:
+        f(*args)
+    fork(*table[1][1][:4], None, None, None, ws)
+    resize(kv, T(9), T(5), T(6), None, None, ws)
+    compact(kv, T(4), T(7), T(2), None, ws)
+    assert len(calls) == 7
+    unfit = [cache(scales=T(255, 32, dtype=u8)), cache(keys=T(255, 64, dtype=u8)), cache(table=T(3, 8, dtype=i64)),
+             cache(lens=T(3, dtype=i64)), cache(lens=T(2))]
+    for f, args, least in table:
+        for i in range(1, len(args) - (f is not copy)):
+            for bad in [T(*args[i].shape, dtype=i64)] + ([T(args[i].shape[0] - 1)] if i in least else []):
+                with pytest.raises(ValueError):
+                    f(*args[:i], bad, *args[i + 1:])
+        for bad in unfit:
+            with pytest.raises(ValueError):
+                f(bad, *args[1:])
+    assert len(calls) == 7
+
+
+def test_the_binding_checks_the_prefix_attention(binding, calls):
+    import torch
+    T = _Tensor
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    kv = binding.KvCache(T(256, 256, dtype=u8), T(256, 32, dtype=u8), None, T(3, 8), T(3), 64)
+    fine = dict(q_bf16=T(6, 4, 512, dtype=bf16), q_per_seq=2, kv=kv, members=T(3), group_begin=T(3), prefix_len=T(2), q_limit=T(6),
+                swa=T(3, 9, 512, dtype=u8), swa_seq_stride=9, swa_begin=T(6), swa_end=T(6), w_max=8, softmax_scale=0.1,
+                o_bf16=T(6, 4, 512, dtype=bf16), lse=T(6, 4, dtype=f32), ws=T(1 << 20, dtype=u8))
+    f = binding.csa2_prefix_attn_decode
+    f(**fine)
+    f(**{**fine, "q_limit": None, "lse": None})
+    f(**{**fine, "swa": None, "swa_seq_stride": 0, "swa_begin": None, "swa_end": None, "w_max": 0})
+    assert len(calls) == 3
+    i64 = torch.int64
+    for name, bad in [("q_bf16", T(6, 4, 512, dtype=f32)), ("q_bf16", T(6, 4, 256, dtype=bf16)), ("members", T(3, dtype=i64)),
+                      ("group_begin", T(2)), ("group_begin", T(3, dtype=i64)), ("prefix_len", T(2, dtype=i64)), ("q_limit", T(5)),
+                      ("q_limit", T(6, dtype=i64)), ("swa", T(3, 8, 512, dtype=u8)), ("swa_begin", T(5)), ("swa_end", T(6, dtype=f32)),
+                      ("o_bf16", T(6, 4, 512, dtype=f32)), ("o_bf16", T(5, 4, 512, dtype=bf16)), ("lse", T(6, 4, dtype=bf16)),
+                      ("lse", T(6, 3, dtype=f32))]:
+        with pytest.raises(ValueError):
+            f(**{**fine, name: bad})
+    assert len(calls) == 3
