@@ -373,3 +373,40 @@ def test_more_than_65535_queries(B, cuda_device):
             got = lse[u].double().cpu().numpy()
             assert (got == wl).all() if np.isinf(wl).any() else (np.abs(got - wl) <= tl).all()
     assert not (o == 77.0).all(-1).any()
+
+
+@pytest.mark.parametrize("members,qps", [(1024, 1), (1025, 1), (512, 2), (205, 5), (1250, 2)])
+def test_queries_around_the_plans_block(B, cuda_device, members, qps):
+    """More queries than the plan's block has threads; many of them have no rows of their own."""
+    third = members // 3
+    _run(B, Case(cuda_device, [third, members - third], [65, 40], [0, 0, 3, 0, 40, 0, 0], 2, 32, qps=qps, seed=members + qps))
+
+
+@pytest.mark.parametrize("groups", [1023, 1024, 1025, 1500])
+def test_groups_around_the_plans_block(B, cuda_device, groups):
+    """As many groups as the plan keeps in shared memory, and more: most of one member, some empty, runs of them
+    without a prefix, and sequences without entries."""
+    sizes = [0 if g % 7 == 3 else 3 if g % 11 == 5 else 1 for g in range(groups)]
+    prefix = [0 if g % 5 == 0 or 300 <= g < 420 or g > groups - 9 else 1 + g % (90 if sizes[g] else 30)
+              for g in range(groups)]
+    _run(B, Case(cuda_device, sizes, prefix, [0, 2, 0, 0, 35], 2, 32, seed=groups))
+
+
+@pytest.mark.parametrize("value", [65536.0, -65536.0, 3e38, -3e38, math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("at", [0, 511, 100, 101])
+def test_out_of_range_q_is_reported(B, cuda_device, value, at):
+    """Either half of a packed pair; the largest value in range is not reported, nor are queries that no group lists."""
+    c = Case(cuda_device, [3], [90], [20], 16, 64, seed=24)
+    c.run(B)
+    assert B.csa2_device_status() == 0
+    q = c.args[0]
+    q[int(c.members[1]), 5, at] = 65280.0  # the bf16 value below 65536
+    B.csa2_prefix_attn_decode(*c.args)
+    assert B.csa2_device_status() == 0
+    spare = (set(range(c.batch)) - set(c.members.tolist())).pop()
+    q[spare, 5, at] = value
+    B.csa2_prefix_attn_decode(*c.args)
+    assert B.csa2_device_status() == 0
+    q[int(c.members[1]), 5, at] = value
+    B.csa2_prefix_attn_decode(*c.args)
+    assert B.csa2_device_status() == 8
