@@ -410,3 +410,23 @@ def test_out_of_range_q_is_reported(B, cuda_device, value, at):
     q[int(c.members[1]), 5, at] = value
     B.csa2_prefix_attn_decode(*c.args)
     assert B.csa2_device_status() == 8
+
+
+@pytest.mark.parametrize("qps,cut", [(2, 1), (4, 3), (7, 2)])
+def test_fewer_queries_of_the_last_sequence(B, cuda_device, qps, cut):
+    """nq that q_per_seq does not divide: what lies behind the last query is neither read nor written."""
+    c = Case(cuda_device, [2, 3], [70, 300], [3, 90, 0], 16, 64, qps=qps, w=20, seed=25, spare=0, limits=lambda rng, n: int(rng.integers(1, n + 1)))
+    full = c.nq
+    c.nq -= cut
+    for name in ("q", "limit", "wb", "we"):
+        setattr(c, name, getattr(c, name)[:c.nq])
+    o, lse = c.run(B)
+    assert B.csa2_device_status() == 0
+    seen = 0
+    for j in range(len(c.members)):
+        for u in range(c.members[j] * qps, min(c.nq, (c.members[j] + 1) * qps)):
+            want, wl, tol, tl = ref.attend(c.q[u].double().numpy(), c.rows(j, u), c.scale)
+            assert (np.abs(o[u].double().cpu().numpy() - want) <= tol).all()
+            assert (np.abs(lse[u].double().cpu().numpy() - wl) <= tl).all()
+            seen += 1
+    assert seen == full - cut
